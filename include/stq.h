@@ -246,6 +246,90 @@ stq_status stq_check_slot_ids(const stq_pool *pool, int32_t B, const int32_t *h_
 stq_status stq_allocate_bits(int32_t n_units, const float *gate_mean, const float *state_msq,
                              double avg_bits, int32_t n_pivots, uint8_t *unit_bits);
 
+/* ------------------------------------------------------------------------
+ * Sequences: the same gated delta rule over many tokens per request, on fp32
+ * states.  A rule is the geometry of one layer; it needs no layout.  Packed
+ * batches: the tokens of B sequences stand back to back,
+ *   d_cu_seqlens [B+1] int32  device; sequence b is the tokens
+ *                             [cu[b], cu[b+1]) of the N that the call is given.
+ *                             Not decreasing, in [0, N]; entries are clamped to
+ *                             that range (and to not decreasing) on the device,
+ *                             so a bad table gives wrong values but no access
+ *                             outside the arrays.  Sequences may be empty.
+ *   d_q, d_k [N,H,d_k], d_v [N,H,d_v]  io_dtype
+ *   d_a      [N,H] fp32 (scalar gate) or [N,H,d_k] fp32 (key-vector gate), in
+ *            [0, 1]; a gate of 0 resets the state exactly
+ *   d_beta   [N,H] fp32 write strengths
+ * Tokens outside every sequence are not read, and their outputs keep what
+ * they held.  Inputs are finite; a NaN or infinity reaches only the outputs of its own
+ * sequence and head.  States are [.,H,d_k,d_v] fp32, key-row-major, as
+ * stq_pack and stq_unpack take them.
+ * Per token: S' = diag(a) S, u = beta (v - S'^T k), S = S' + k u^T, o = S^T q.
+ */
+typedef struct {
+    int32_t H;               /* heads, 1..4096 */
+    int32_t d_k, d_v;        /* 64 or 128 each */
+    int32_t gate;            /* STQ_GATE_SCALAR | STQ_GATE_KEYVEC */
+    int32_t io_dtype;        /* STQ_BF16 | STQ_F32: q, k, v and their gradients */
+} stq_rule;
+
+/*
+ * The rule token by token, for one or a few tokens per request, on stored
+ * states d_state [slots,H,d_k,d_v] fp32, updated in place:
+ *   d_slot_ids [B] int32 device, distinct; NULL: sequence b uses slot b.  A
+ *              request whose id is out of [0, slots) gets NaN outputs and
+ *              changes no state.
+ *   d_commit   [B] int32 device, NULL: how many of a request's leading tokens
+ *              the stored state takes in (clamped to [0, its length]); the
+ *              others are run ahead of it, for drafted tokens that may yet be
+ *              rejected.  NULL: all tokens.  0: the state is not written.
+ *   d_o        [N,H,d_v] fp32 output of every token
+ * One read and at most one write of each state; fp32 arithmetic in a fixed
+ * order.  Meant for up to about sixteen tokens a request; longer sequences are
+ * right too, and faster with stq_chunk_forward.  Allocates nothing, does not
+ * synchronize, may be captured in a HIP graph.
+ * Errors: STQ_ERR_INVALID (NULL, B or N negative, B > slots, a bad rule),
+ * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128), STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ */
+stq_status stq_recurrent_step(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
+                              const void *d_q, const void *d_k, const void *d_v, const float *d_a,
+                              const float *d_beta, float *d_state, int32_t slots,
+                              const int32_t *d_slot_ids, const int32_t *d_commit, float *d_o,
+                              void *stream);
+
+/* Bytes of device workspace that stq_verify_draft needs for B requests over a
+ * vocabulary of V tokens. */
+stq_status stq_verify_workspace(int32_t B, int32_t V, size_t *bytes);
+
+/*
+ * Acceptance of drafted tokens by the target's probabilities, from given
+ * random numbers (the rejection scheme of speculative sampling: the emitted
+ * tokens are distributed as the target's).  Per request, with n drafted tokens
+ * x_0..x_{n-1}, target rows p_0..p_n and draft rows q_0..q_{n-1}:
+ *   token t stands while r_t * q_t(x_t) < p_t(x_t), compared exactly;
+ *   n_accepted = the number of leading tokens that stand;
+ *   next_token = the smallest i with sum_{j<=i} w_j > r_T * sum_j w_j, where
+ *     w = max(p_t - q_t, 0) of the first token t that does not stand, or p_n
+ *     if all stand (p_t also where max(p_t - q_t, 0) is 0 everywhere).
+ * Sums are in 64 bits, in an order fixed by V, so a request's result does not
+ * depend on its batch.  A weight that is NaN counts as 0; next_token is -1
+ * where every weight is 0.  A drafted token outside [0, V) does not stand.
+ *   d_draft_tokens [B,T] int32; d_draft_len [B] int32 in [0, T] (clamped;
+ *   NULL: T each); d_target [B,T+1,V], d_draft [B,T,V] dtype (STQ_F32 |
+ *   STQ_BF16); d_uniform [B,T+1] fp32 in [0, 1): r_t, and r_T for next_token;
+ *   d_n_accepted, d_next_token [B] int32 outputs.
+ * T may be 0 (d_draft_tokens and d_draft may be NULL): next_token is sampled
+ * from d_target.  Allocates nothing, does not synchronize, may be captured.
+ * A workspace must not be used by two calls that overlap in time.
+ * Errors: STQ_ERR_INVALID (NULL, B, T or V out of range, a bad dtype),
+ * STQ_ERR_TOO_SMALL (workspace), STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ */
+stq_status stq_verify_draft(int32_t B, int32_t T, int32_t V, int32_t dtype,
+                            const int32_t *d_draft_tokens, const int32_t *d_draft_len,
+                            const void *d_target, const void *d_draft, const float *d_uniform,
+                            int32_t *d_n_accepted, int32_t *d_next_token, void *d_workspace,
+                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

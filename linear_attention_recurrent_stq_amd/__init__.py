@@ -6,7 +6,8 @@ and the stream.  Importing this package fails loudly when the library is not
 built; there is no fallback.
 
 Names follow the C ABI in ``include/stq.h``: ``Layout`` (stq_pack_layout),
-``Pool`` (stq_alloc_pool), ``decode_step``, ``unpack``, ``pack``.
+``Pool`` (stq_alloc_pool), ``decode_step``, ``unpack``, ``pack``; over several
+tokens of each sequence: ``recurrent_step``, ``verify_draft``.
 """
 from __future__ import annotations
 
@@ -35,7 +36,8 @@ FIT_STEP, FIT_LAGGED = 0, 1
 
 SYMBOLS = ["stq_status_string", "stq_last_error", "stq_pack_layout", "stq_layout_query",
            "stq_layout_head", "stq_layout_free", "stq_alloc_pool", "stq_decode_step",
-           "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids", "stq_allocate_bits"]
+           "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids", "stq_allocate_bits",
+           "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft"]
 
 
 class StqConfig(C.Structure):
@@ -51,7 +53,13 @@ class StqPool(C.Structure):
                 ("layout", C.c_void_p)]
 
 
+class StqRule(C.Structure):
+    _fields_ = [("H", C.c_int32), ("d_k", C.c_int32), ("d_v", C.c_int32), ("gate", C.c_int32),
+                ("io_dtype", C.c_int32)]
+
+
 _P = C.c_void_p
+_I = C.c_int32
 _lib.stq_status_string.restype = C.c_char_p
 _lib.stq_status_string.argtypes = [C.c_int]
 _lib.stq_last_error.restype = C.c_char_p
@@ -68,9 +76,12 @@ _lib.stq_pack.argtypes = [C.POINTER(StqPool), C.c_int32, _P, _P, _P]
 _lib.stq_allocate_bits.argtypes = [C.c_int32, _P, _P, C.c_double, C.c_int32, _P]
 _lib.stq_check_slot_ids.argtypes = [C.POINTER(StqPool), C.c_int32, _P]
 _lib.stq_fit_scales.argtypes = [C.POINTER(StqPool), C.c_int32, _P, _P]
+_lib.stq_recurrent_step.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 7 + [_I] + [_P] * 4
+_lib.stq_verify_workspace.argtypes = [_I, _I, C.POINTER(C.c_size_t)]
+_lib.stq_verify_draft.argtypes = [_I] * 4 + [_P] * 8 + [C.c_size_t, _P]
 for _f in ("stq_pack_layout", "stq_layout_query", "stq_layout_head", "stq_alloc_pool",
            "stq_decode_step", "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids",
-           "stq_allocate_bits"):
+           "stq_allocate_bits", "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -305,3 +316,112 @@ def calibrate(H, d_k, d_v, *, B, steps, inputs, unit=UNIT_HEAD, gate=GATE_SCALAR
         gate_mean = g.mean(axis=1)
         state_msq = m.mean(axis=1)
     return gate_mean.astype(np.float32), state_msq.astype(np.float32)
+
+
+# ------------------------------------------------------------- sequences
+
+def _rule(q, v, a):
+    """stq_rule of packed inputs q [N,H,d_k], v [N,H,d_v], a [N,H] or [N,H,d_k]."""
+    import torch
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k must be [N,H,d_k] and v [N,H,d_v]")
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    return StqRule(q.shape[1], q.shape[2], v.shape[2], GATE_KEYVEC if a.dim() == 3 else GATE_SCALAR,
+                   BF16 if q.dtype == torch.bfloat16 else F32)
+
+
+def _one_device(ref, **tensors):
+    """Every given tensor on the device of `ref`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+def _seq_inputs(cu_seqlens, q, k, v, a, beta):
+    """Checks a packed batch and returns (rule, B, N, pointers of cu, q, k, v, a, beta)."""
+    import torch
+    rule = _rule(q, v, a)
+    N, H, dk = q.shape
+    dv, io = v.shape[2], q.dtype
+    if tuple(k.shape) != (N, H, dk) or tuple(v.shape) != (N, H, dv):
+        raise ValueError("q, k must be [N,H,d_k] and v [N,H,d_v]")
+    if tuple(a.shape) not in ((N, H), (N, H, dk)) or tuple(beta.shape) != (N, H):
+        raise ValueError("a must be [N,H] or [N,H,d_k], beta [N,H]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [B+1]")
+    _one_device(q, cu_seqlens=cu_seqlens, k=k, v=v, a=a, beta=beta)
+    return rule, cu_seqlens.numel() - 1, N, [
+        _dptr(cu_seqlens, "cu_seqlens", torch.int32), _dptr(q, "q"), _dptr(k, "k", io), _dptr(v, "v", io),
+        _dptr(a, "a", torch.float32), _dptr(beta, "beta", torch.float32)]
+
+
+def _opt(t, what, dtype):
+    return None if t is None else _dptr(t, what, dtype)
+
+
+def recurrent_step(state, slot_ids, cu_seqlens, q, k, v, a, beta, o, commit=None, stream=None) -> None:
+    """stq_recurrent_step on torch device tensors: the tokens of B packed
+    sequences through the fp32 states [slots,H,d_k,d_v] in place (slot_ids
+    None: sequence b uses slot b); o [N,H,d_v] fp32.  commit [B] int32: how many
+    leading tokens of each request its state takes in (None: all)."""
+    import torch
+    rule, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (rule.H, rule.d_k, rule.d_v):
+        raise ValueError("state must be [slots,H,d_k,d_v]")
+    if tuple(o.shape) != (N, rule.H, rule.d_v):
+        raise ValueError("o must be [N,H,d_v]")
+    for t, what in ((slot_ids, "slot_ids"), (commit, "commit")):
+        if t is not None and tuple(t.shape) != (B,):
+            raise ValueError(f"{what} must be [B]")
+    _one_device(q, state=state, slot_ids=slot_ids, commit=commit, o=o)
+    with torch.cuda.device(q.device):
+        _check(_lib.stq_recurrent_step(
+            C.byref(rule), B, N, *ptrs, _dptr(state, "state", torch.float32), state.shape[0],
+            _opt(slot_ids, "slot_ids", torch.int32), _opt(commit, "commit", torch.int32),
+            _dptr(o, "o", torch.float32), _stream_ptr(stream)), "stq_recurrent_step")
+
+
+class VerifyPlan:
+    """Sizes and workspace of verify_draft: up to max_requests requests of up to
+    max_draft drafted tokens over a vocabulary of V, probabilities of `dtype`
+    (F32 or BF16).  A plan must not be used by two calls that overlap in time."""
+
+    def __init__(self, max_requests, max_draft, V, dtype=F32, device="cuda"):
+        import torch
+        n = C.c_size_t()
+        _check(_lib.stq_verify_workspace(max_requests, V, C.byref(n)), "stq_verify_workspace")
+        self.max_requests, self.max_draft, self.V, self.dtype = max_requests, max_draft, V, dtype
+        self.workspace = torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+
+
+def verify_draft(plan: VerifyPlan, draft_tokens, target, draft, uniform, n_accepted, next_token, *,
+                 draft_len=None, stream=None) -> None:
+    """stq_verify_draft on torch device tensors: draft_tokens [B,T] int32,
+    target [B,T+1,V], draft [B,T,V], uniform [B,T+1] fp32 in [0, 1), draft_len
+    [B] int32 or None; writes n_accepted and next_token [B] int32.  With T = 0
+    (draft_tokens and draft of no elements) next_token is drawn from target."""
+    import torch
+    io = torch.bfloat16 if plan.dtype == BF16 else torch.float32
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be [B,T]")
+    B, T = draft_tokens.shape
+    if B > plan.max_requests or T > plan.max_draft:
+        raise ValueError("the batch exceeds the plan")
+    if (tuple(target.shape) != (B, T + 1, plan.V) or tuple(draft.shape) != (B, T, plan.V)
+            or tuple(uniform.shape) != (B, T + 1)):
+        raise ValueError("target must be [B,T+1,V], draft [B,T,V], uniform [B,T+1]")
+    for t, what in ((n_accepted, "n_accepted"), (next_token, "next_token"), (draft_len, "draft_len")):
+        if t is not None and tuple(t.shape) != (B,):
+            raise ValueError(f"{what} must be [B]")
+    _one_device(target, draft_tokens=draft_tokens, draft=draft, uniform=uniform, n_accepted=n_accepted,
+                next_token=next_token, draft_len=draft_len, workspace=plan.workspace)
+    i32 = torch.int32
+    with torch.cuda.device(target.device):
+        _check(_lib.stq_verify_draft(
+            B, T, plan.V, plan.dtype, _dptr(draft_tokens, "draft_tokens", i32) if T else None,
+            _opt(draft_len, "draft_len", i32), _dptr(target, "target", io),
+            _dptr(draft, "draft", io) if T else None, _dptr(uniform, "uniform", torch.float32),
+            _dptr(n_accepted, "n_accepted", i32), _dptr(next_token, "next_token", i32),
+            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
+            "stq_verify_draft")

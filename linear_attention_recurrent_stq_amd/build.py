@@ -2,7 +2,7 @@
 
 Each source is compiled to an object of its own (in parallel, under
 ``_build/``) and the objects are linked into the shared library.  The same
-kernels are also linked with the host source built with STQ_DEBUG_VALIDATE
+kernels are also linked with the host sources built with STQ_DEBUG_VALIDATE
 into ``libstq_debug.so``: there every call that takes slot ids copies them to
 the host and rejects duplicates and out-of-range ids before any launch.
 
@@ -28,7 +28,9 @@ SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined
        "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = [os.path.join(HERE, "csrc", f)
-           for f in ("stq_host.cpp", "stq_alloc.cpp", "stq_kernels.hip", "stq_window.hip")]
+           for f in ("stq_host.cpp", "stq_seq_host.cpp", "stq_alloc.cpp", "stq_kernels.hip",
+                     "stq_window.hip", "stq_recurrent.hip", "stq_verify.hip")]
+VALIDATING = 2  # the first sources: their debug build validates slot ids
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -50,7 +52,7 @@ def _jobs() -> int:
         n = len(os.sched_getaffinity(0))
     except AttributeError:
         n = os.cpu_count() or 1
-    return max(1, min(16, n, len(SOURCES) + 1))
+    return max(1, min(16, n, len(SOURCES) + VALIDATING))
 
 
 def build(verbose: bool = False) -> str:
@@ -58,10 +60,9 @@ def build(verbose: bool = False) -> str:
     recompiles).  Returns the path of libstq.so."""
     os.makedirs(OBJDIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include")]
-    host = SOURCES[0]
     jobs = [(src, os.path.join(OBJDIR, os.path.basename(src) + ".o"), []) for src in SOURCES]
-    jobs.append((host, os.path.join(OBJDIR, "debug_" + os.path.basename(host) + ".o"),
-                 ["-DSTQ_DEBUG_VALIDATE=1"]))
+    jobs += [(src, os.path.join(OBJDIR, "debug_" + os.path.basename(src) + ".o"),
+              ["-DSTQ_DEBUG_VALIDATE=1"]) for src in SOURCES[:VALIDATING]]
 
     def compile_one(job):
         src, obj, extra = job
@@ -76,7 +77,8 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(_jobs()) as ex:
         list(ex.map(compile_one, order))
     objs = [j[1] for j in jobs]
-    for out, use in ((LIB, objs[:len(SOURCES)]), (LIB_DEBUG, [objs[-1]] + objs[1:len(SOURCES)])):
+    release, debug = objs[:len(SOURCES)], objs[len(SOURCES):]
+    for out, use in ((LIB, release), (LIB_DEBUG, debug + release[VALIDATING:])):
         tmp = out + ".tmp%d" % os.getpid()
         cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *use, "-o", tmp]
         if verbose:

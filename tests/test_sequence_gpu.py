@@ -1,0 +1,221 @@
+"""The sequence operators against plain 64-bit references, at the sizes, masks
+and tables where they can go wrong."""
+import numpy as np
+import pytest
+import torch  # before the library: both then use the HIP runtime that torch loads
+
+from tests import seqref
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24   # half a step of fp32, relative
+
+
+@pytest.fixture(scope="module")
+def stq():
+    import linear_attention_recurrent_stq_amd as m
+    return m
+
+
+def _inputs(rng, n, H, dk, dv, keyvec, bf16, lo=0.7):
+    """Packed inputs as torch device tensors and as the numpy values they hold."""
+    def dev(x, t):
+        y = torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(t)
+        return y.cuda(), y.double().numpy()
+    io = torch.bfloat16 if bf16 else torch.float32
+    unit = lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True)
+    x = {"q": dev(unit(rng.normal(size=(n, H, dk))), io), "k": dev(unit(rng.normal(size=(n, H, dk))), io),
+         "v": dev(rng.normal(size=(n, H, dv)), io),
+         "a": dev(rng.uniform(lo, 1, (n, H, dk) if keyvec else (n, H)), torch.float32),
+         "beta": dev(rng.uniform(0, 1, (n, H)), torch.float32)}
+    return {m: y[0] for m, y in x.items()}, {m: y[1] for m, y in x.items()}
+
+
+def _dev(x, t):
+    return torch.from_numpy(np.asarray(x)).to(t).cuda()
+
+
+def _cu(lens):
+    at = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    return at, torch.from_numpy(at).cuda()
+
+
+def _rel(got, want):
+    """Distance over the reference's norm, over all elements."""
+    n = np.linalg.norm(want)
+    return np.linalg.norm(np.asarray(got, np.float64) - want) / n if n else np.abs(got).max()
+
+
+# ---------------------------------------------------------------- recurrent
+# A token's sums have d_k / 8 terms in a lane and three cross-lane adds, then
+# four more roundings: an error of at most (d_k / 8 + 7) E32 of the state's and
+# the token's norm enters per token.  With |k| <= 1, beta <= 1 and a <= 1 the
+# update does not enlarge an error of the state, so after T tokens it is within
+# T times that; outputs are the state times |q| = 1.  The norms of state and
+# tokens are of one size here, hence the factor 4 against the norm of the result.
+def _step_tol(dk, T):
+    return 4 * T * (dk / 8 + 7) * E32
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("keyvec,bf16", [(False, False), (False, True), (True, False), (True, True)])
+def test_recurrent(stq, dk, dv, keyvec, bf16):
+    rng = np.random.default_rng(dk + dv)
+    lens, H, slots = [1, 0, 5, 16, 2], 3, 7
+    at, cu = _cu(lens)
+    n = at[-1] + 3                       # three tokens behind the last sequence
+    x, y = _inputs(rng, n, H, dk, dv, keyvec, bf16)
+    ids = np.array([4, 0, 6, 1, 3], np.int32)
+    S0 = rng.normal(size=(slots, H, dk, dv)).astype(np.float32)
+    commit = np.array([1, 0, 2, 99, -1], np.int32)
+    o = torch.full((n, H, dv), 7.0, device="cuda")
+    for given in (None, commit):
+        S = torch.from_numpy(S0).cuda()
+        stq.recurrent_step(S, _dev(ids, torch.int32), cu, x["q"], x["k"], x["v"], x["a"], x["beta"], o,
+                           commit=None if given is None else _dev(given, torch.int32))
+        wo, last, kept = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), S0[ids],
+                                        np.clip(commit, 0, lens))
+        want = S0.astype(np.float64)
+        want[ids] = last if given is None else kept
+        go, gS = o.cpu().numpy(), S.cpu().numpy()
+        assert (go[at[-1]:] == 7).all()
+        assert _rel(go[:at[-1]], wo[:at[-1]]) < _step_tol(dk, max(lens))
+        assert _rel(gS, want) < _step_tol(dk, max(lens))
+        for s in range(slots):           # untouched slots keep their bits
+            if s not in ids or lens[list(ids).index(s)] == 0 or (given is not None and s == 3):
+                assert np.array_equal(gS[s], S0[s]), s
+
+
+def test_recurrent_equals_single_tokens_and_decode(stq):
+    """Several tokens in one call, the same tokens one call each, and the
+    decode step on fp32 units: the first two are the same bits, the third the
+    same rule in another order of sums."""
+    rng = np.random.default_rng(3)
+    H, d, T, B = 4, 128, 4, 3
+    at, cu = _cu([T] * B)
+    x, y = _inputs(rng, T * B, H, d, d, True, True)
+    S0 = torch.from_numpy(rng.normal(size=(B, H, d, d)).astype(np.float32)).cuda()
+    S, o = S0.clone(), torch.empty(T * B, H, d, device="cuda")
+    stq.recurrent_step(S, None, cu, x["q"], x["k"], x["v"], x["a"], x["beta"], o)
+    L = stq.Layout(H, d, d, np.full(H, 32, np.uint8), gate=stq.GATE_KEYVEC)
+    pool = stq.Pool(L, B)
+    ids = torch.arange(B, dtype=torch.int32, device="cuda")
+    stq.pack(pool, ids, S0)
+    S1, one, od = S0.clone(), torch.empty(B, H, d, device="cuda"), torch.empty(B, H, d, device="cuda")
+    cu1 = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    for t in range(T):
+        z = {m: x[m].view(B, T, *x[m].shape[1:])[:, t].contiguous() for m in x}
+        stq.recurrent_step(S1, ids, cu1, z["q"], z["k"], z["v"], z["a"], z["beta"], one)
+        assert torch.equal(one, o.view(B, T, H, d)[:, t])
+        stq.decode_step(pool, ids, z["q"], z["k"], z["v"], z["a"], z["beta"], od)
+        assert _rel(od.cpu().numpy(), one.double().cpu().numpy()) < 2 * _step_tol(d, T)
+    assert torch.equal(S, S1)
+
+
+@pytest.mark.parametrize("keyvec", [False, True])
+def test_recurrent_resets_and_bad_slots(stq, keyvec):
+    """Gates of 0 drop the state exactly, beta 0 writes nothing, a slot id out
+    of range gives NaN outputs and leaves every state."""
+    rng = np.random.default_rng(5)
+    H, d = 2, 64
+    at, cu = _cu([3, 2, 1])
+    x, y = _inputs(rng, 6, H, d, d, keyvec, False)
+    x["a"][1] = 0
+    x["beta"][2] = 0
+    x["v"][5] = 0
+    x["beta"][3:] = 0
+    S0 = torch.from_numpy(rng.normal(size=(3, H, d, d)).astype(np.float32)).cuda()
+    S, o = S0.clone(), torch.empty(6, H, d, device="cuda")
+    stq.recurrent_step(S, _dev(np.array([2, 3, 0], np.int32), torch.int32), cu, x["q"], x["k"], x["v"], x["a"],
+                       x["beta"], o)
+    assert torch.isnan(o[3:5]).all() and torch.equal(S[1], S0[1])
+    # after the reset the state is k u^T of that token alone, then decayed
+    a2 = x["a"][2][:, :, None] if keyvec else x["a"][2][:, None, None]
+    u = x["beta"][1][:, None] * x["v"][1]
+    want = a2 * (x["k"][1][:, :, None] * u[:, None, :])
+    assert torch.equal(S[2], want)
+    a5 = x["a"][5][:, :, None] if keyvec else x["a"][5][:, None, None]
+    assert torch.equal(S[0], a5 * S0[0])
+
+
+def test_recurrent_python_refusals(stq):
+    H, d = 2, 64
+    x, _ = _inputs(np.random.default_rng(0), 2, H, d, d, False, False)
+    S, o = torch.zeros(2, H, d, d, device="cuda"), torch.zeros(2, H, d, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    good = dict(state=S, slot_ids=None, cu_seqlens=cu, o=o, **x)
+    for bad in (dict(state=S[0]), dict(o=o.double()), dict(cu_seqlens=cu.long()), dict(cu_seqlens=cu.cpu()),
+                dict(k=x["k"].bfloat16()), dict(q=x["q"].half()), dict(v=x["v"].transpose(1, 2)),
+                dict(beta=x["beta"][:1]), dict(commit=cu), dict(slot_ids=cu), dict(state=S[:1]), dict(o=o.cpu())):
+        with pytest.raises((ValueError, stq.StqError)):
+            stq.recurrent_step(**{**good, **bad})
+    stq.recurrent_step(**good)
+
+
+# ------------------------------------------------------------------- verify
+
+def _probs(rng, shape, bf16, hot=2.0):
+    x = torch.softmax(torch.from_numpy(rng.normal(size=shape) * hot), -1)
+    return x.to(torch.bfloat16 if bf16 else torch.float32)
+
+
+def _run_verify(stq, tok, lens, p, q, r):
+    B, T = tok.shape
+    plan = stq.VerifyPlan(B, T, p.shape[2], stq.BF16 if p.dtype == torch.bfloat16 else stq.F32)
+    acc = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    nxt = acc.clone()
+    stq.verify_draft(plan, _dev(tok, torch.int32), p.cuda(), q.cuda(), _dev(r, torch.float32), acc, nxt,
+                     draft_len=None if lens is None else _dev(lens, torch.int32))
+    return acc.cpu().numpy(), nxt.cpu().numpy()
+
+
+@pytest.mark.parametrize("B,T,V,bf16", [(1, 1, 1, False), (5, 3, 7, False), (33, 5, 1000, True), (4, 2, 2048, False),
+                                        (7, 4, 2049, True), (3, 70, 50, False), (6, 3, 131073, False)])
+def test_verify(stq, B, T, V, bf16):
+    rng = np.random.default_rng(B * 1000 + V)
+    p, q = _probs(rng, (B, T + 1, V), bf16), _probs(rng, (B, T, V), bf16)
+    q = ((q.double() + 3 * p[:, :T].double()) / 4).to(p.dtype)      # mostly agreeing
+    tok = rng.integers(0, V, (B, T)).astype(np.int32)
+    lens = rng.integers(-1, T + 2, B).astype(np.int32)
+    r = rng.uniform(size=(B, T + 1)).astype(np.float32)
+    for given in (None, lens):
+        acc, nxt = _run_verify(stq, tok, given, p, q, r)
+        want = seqref.verify(tok, given, p.double().numpy(), q.double().numpy(), r)
+        assert np.array_equal(acc, want[0]) and np.array_equal(nxt, want[1])
+
+
+def test_verify_edges(stq):
+    """Draws of 0 and next to 1, equal rows, one-hot rows, rows of no mass,
+    NaN weights, tokens outside the vocabulary, draft probability 0."""
+    V, T, B = 300, 2, 9
+    p, q = torch.zeros(B, T + 1, V), torch.zeros(B, T, V)
+    p[:, :, 10], p[:, :, 200] = 0.25, 0.75
+    q[:, :, 10], q[:, :, 200] = 0.75, 0.25
+    tok = np.full((B, T), 10, np.int32)
+    r = np.full((B, T + 1), 0.5, np.float32)      # 0.5 * 0.75 < 0.25 fails: rejected, rest is 200
+    r[1, 0] = np.nextafter(np.float32(1 / 3), np.float32(0))  # just accepted
+    r[2, 2] = 0.0
+    q[3] = p[3, :T]                                # equal rows: r q < p always holds
+    r[3, 2] = np.nextafter(np.float32(1), np.float32(0))
+    tok[4] = [-1, 10]
+    tok[5] = [V, 10]
+    p[6] = 0
+    q[7, :, 10] = 0                                # draft probability 0 but target's not: stands
+    p[8, 0, 11] = float("nan")
+    q[8, 0] = 1.0                                  # nothing left over: p itself, NaN as 0
+    acc, nxt = _run_verify(stq, tok, None, p, q, r)
+    want = seqref.verify(tok, None, p.double().numpy(), q.double().numpy(), r)
+    assert np.array_equal(acc, want[0]) and np.array_equal(nxt, want[1])
+    assert list(nxt[:1]) == [200] and nxt[2] == 200 and acc[3] == 2 and nxt[3] == 200
+    assert acc[4] == 0 and acc[5] == 0 and nxt[6] == -1 and acc[7] == 2
+
+
+def test_verify_sampling_without_drafts(stq):
+    rng = np.random.default_rng(9)
+    p = _probs(rng, (40, 1, 5000), False)
+    r = rng.uniform(size=(40, 1)).astype(np.float32)
+    tok, q = np.zeros((40, 0), np.int32), p[:, :0]
+    acc, nxt = _run_verify(stq, tok, None, p, q, r)
+    assert (acc == 0).all()
+    c = np.cumsum(p[:, 0].double().numpy(), -1)
+    assert np.array_equal(nxt, (c <= r.astype(np.float64) * c[:, -1:]).sum(-1))
