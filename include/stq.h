@@ -297,6 +297,34 @@ stq_status stq_recurrent_step(const stq_rule *rule, int32_t B, int32_t N, const 
                               const int32_t *d_slot_ids, const int32_t *d_commit, float *d_o,
                               void *stream);
 
+/* Bytes of device workspace that stq_chunk_forward (backward = 0) or
+ * stq_chunk_backward (backward = 1) needs for at most B sequences of at most N
+ * tokens together; it grows with both. */
+stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32_t backward,
+                               size_t *bytes);
+
+/*
+ * The rule over whole sequences (prefill, training's forward pass), by chunks
+ * of 64 tokens on the matrix units:
+ *   d_initial [B,H,d_k,d_v] fp32 states before the first tokens, NULL: zero
+ *   d_final   [B,H,d_k,d_v] fp32 states after the last tokens, NULL: not
+ *             wanted; may be d_initial.  An empty sequence passes its state on.
+ *   d_o       [N,H,d_v] io_dtype
+ * States and sums are fp32; products take fp32 operands as scaled fp16 pairs
+ * (22 bits), so results are those of fp32 arithmetic to a few ulp of their
+ * row's and column's norm.  Results do not depend on the batch around a
+ * sequence's place in its chunks of 64, and are the same at every run.
+ * Allocates nothing, does not synchronize, may be captured in a HIP graph.  A
+ * workspace must not be used by two calls that overlap in time.
+ * Errors: STQ_ERR_INVALID (NULL, B or N negative, a bad rule),
+ * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, B > 65535), STQ_ERR_TOO_SMALL,
+ * STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ */
+stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
+                             const void *d_q, const void *d_k, const void *d_v, const float *d_a,
+                             const float *d_beta, const float *d_initial, void *d_o, float *d_final,
+                             void *d_workspace, size_t workspace_bytes, void *stream);
+
 /* Bytes of device workspace that stq_verify_draft needs for B requests over a
  * vocabulary of V tokens. */
 stq_status stq_verify_workspace(int32_t B, int32_t V, size_t *bytes);

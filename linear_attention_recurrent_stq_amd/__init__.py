@@ -7,7 +7,7 @@ built; there is no fallback.
 
 Names follow the C ABI in ``include/stq.h``: ``Layout`` (stq_pack_layout),
 ``Pool`` (stq_alloc_pool), ``decode_step``, ``unpack``, ``pack``; over several
-tokens of each sequence: ``recurrent_step``, ``verify_draft``.
+tokens of each sequence: ``chunk_forward``, ``recurrent_step``, ``verify_draft``.
 """
 from __future__ import annotations
 
@@ -37,7 +37,8 @@ FIT_STEP, FIT_LAGGED = 0, 1
 SYMBOLS = ["stq_status_string", "stq_last_error", "stq_pack_layout", "stq_layout_query",
            "stq_layout_head", "stq_layout_free", "stq_alloc_pool", "stq_decode_step",
            "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids", "stq_allocate_bits",
-           "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft"]
+           "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft", "stq_chunk_workspace",
+           "stq_chunk_forward"]
 
 
 class StqConfig(C.Structure):
@@ -77,11 +78,14 @@ _lib.stq_allocate_bits.argtypes = [C.c_int32, _P, _P, C.c_double, C.c_int32, _P]
 _lib.stq_check_slot_ids.argtypes = [C.POINTER(StqPool), C.c_int32, _P]
 _lib.stq_fit_scales.argtypes = [C.POINTER(StqPool), C.c_int32, _P, _P]
 _lib.stq_recurrent_step.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 7 + [_I] + [_P] * 4
+_lib.stq_chunk_workspace.argtypes = [C.POINTER(StqRule), _I, _I, _I, C.POINTER(C.c_size_t)]
+_lib.stq_chunk_forward.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 10 + [C.c_size_t, _P]
 _lib.stq_verify_workspace.argtypes = [_I, _I, C.POINTER(C.c_size_t)]
 _lib.stq_verify_draft.argtypes = [_I] * 4 + [_P] * 8 + [C.c_size_t, _P]
 for _f in ("stq_pack_layout", "stq_layout_query", "stq_layout_head", "stq_alloc_pool",
            "stq_decode_step", "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids",
-           "stq_allocate_bits", "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft"):
+           "stq_allocate_bits", "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft",
+           "stq_chunk_workspace", "stq_chunk_forward"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -380,6 +384,60 @@ def recurrent_step(state, slot_ids, cu_seqlens, q, k, v, a, beta, o, commit=None
             C.byref(rule), B, N, *ptrs, _dptr(state, "state", torch.float32), state.shape[0],
             _opt(slot_ids, "slot_ids", torch.int32), _opt(commit, "commit", torch.int32),
             _dptr(o, "o", torch.float32), _stream_ptr(stream)), "stq_recurrent_step")
+
+
+class ChunkPlan:
+    """Rule and workspace of chunk_forward (and, with backward, chunk_backward)
+    for batches of up to max_seqs sequences of up to max_tokens tokens together.
+    A plan must not be used by two calls that overlap in time."""
+
+    def __init__(self, H, d_k, d_v, *, gate=GATE_SCALAR, io_dtype=BF16, max_tokens, max_seqs,
+                 backward=False, device="cuda"):
+        import torch
+        self.rule = StqRule(H, d_k, d_v, gate, io_dtype)
+        self.max_tokens, self.max_seqs, self.backward = max_tokens, max_seqs, bool(backward)
+        n = C.c_size_t()
+        _check(_lib.stq_chunk_workspace(C.byref(self.rule), max_seqs, max_tokens, int(self.backward), C.byref(n)),
+               "stq_chunk_workspace")
+        self.workspace = torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+
+    def inputs(self, cu_seqlens, q, k, v, a, beta):
+        """Checks a packed batch against the plan; returns (B, N, pointers)."""
+        rule, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
+        if bytes(rule) != bytes(self.rule):
+            raise ValueError("the batch's heads, sizes, gate or types are not the plan's")
+        if B > self.max_seqs or N > self.max_tokens:
+            raise ValueError("the batch exceeds the plan")
+        _one_device(q, workspace=self.workspace)
+        return B, N, ptrs
+
+    def states(self, B, ref, **states):
+        """Pointers of states [B,H,d_k,d_v] fp32 (None stays None)."""
+        import torch
+        r = self.rule
+        for name, t in states.items():
+            if t is not None and tuple(t.shape) != (B, r.H, r.d_k, r.d_v):
+                raise ValueError(f"{name} must be [B,H,d_k,d_v]")
+        _one_device(ref, **states)
+        return [_opt(t, name, torch.float32) for name, t in states.items()]
+
+
+def chunk_forward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, o, *, initial_state=None,
+                  final_state=None, stream=None) -> None:
+    """stq_chunk_forward on torch device tensors: packed q, k [N,H,d_k],
+    v [N,H,d_v], a [N,H] or [N,H,d_k], beta [N,H], cu_seqlens [B+1] int32; o
+    [N,H,d_v] as v; states [B,H,d_k,d_v] fp32 (final_state may be initial_state)."""
+    import torch
+    B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
+    if o.shape != v.shape:
+        raise ValueError("o must be [N,H,d_v]")
+    first, last = plan.states(B, q, initial_state=initial_state, final_state=final_state)
+    _one_device(q, o=o)
+    with torch.cuda.device(q.device):
+        _check(_lib.stq_chunk_forward(
+            C.byref(plan.rule), B, N, *ptrs, first, _dptr(o, "o", v.dtype), last,
+            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
+            "stq_chunk_forward")
 
 
 class VerifyPlan:

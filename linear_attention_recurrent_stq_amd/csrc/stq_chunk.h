@@ -1,0 +1,119 @@
+// Shared pieces of the chunked gated delta rule (forward and backward): the
+// chunk table, the scaled fp16 pairs that carry fp32 values through the matrix
+// instructions, and fragment layouts.  Not part of the ABI.
+//
+// A sequence is cut into chunks of 64 tokens.  With G_i the product of the
+// gates of a chunk's tokens up to i (per key channel; one value per token for
+// scalar gates), S0 the state at its start, row-major d_k x d_v:
+//   A_ij = sum_c k_ic k_jc prod_{j<s<=i} a_sc  (i > j)
+//   P_ij = sum_c q_ic k_jc prod_{j<s<=i} a_sc  (i >= j)
+//   T = (I + diag(beta) A)^-1 diag(beta)
+//   u = T (V - (K G) S0);   O = (Q G) S0 + P u;   S1 = diag(G_64) S0 + (K G_64/G)^T u
+// Every gate product, G_64/G_i among them, is formed by multiplying gates, never by a
+// quotient, so gates that underflow, or are 0, are right.
+//
+// Numbers.  States, sums and u are fp32.  A matrix instruction takes an fp32
+// operand x as two fp16 values, x 2^e = hi + lo (22 bits and more), with e
+// chosen per row of a left or per column of a right operand so that its
+// largest value is near 2^10 (left) or 2^14 (right); the product hi hi + hi lo + lo hi
+// leaves out lo lo, at most 2^-22 of the operands' largest values, so results
+// keep fp32's accuracy relative to a row's and column's norm.  bf16 inputs are
+// exact in the hi part alone (a value under 2^-24 of its row's largest loses bits).
+#pragma once
+
+#include "stq_seq.h"
+
+namespace stq {
+
+constexpr int kC = 64;               // tokens of a chunk
+constexpr int kFrag = 512;           // halves of one 16x32 fragment (64 lanes x 8)
+constexpr int kTri = 6;              // 16x32 fragments of a lower triangular 64x64 matrix
+
+// What k_chunk_prep leaves for one (chunk, head): T and P as fragments (hi,
+// then lo), and per-token factors.
+struct ChunkMeta {
+    float sk[kC], sq[kC];            // 2^e of the rows of K and Q
+    float rk[kC], rq[kC];            // factors that undo it (and G_i for scalar gates)
+    float rt[kC], rp[kC];            // factors that undo the row scales of T and P
+    float rw[kC];                    // factor of u_i in the state's update: 2^-e (and G_64/G_i)
+    float dec[128];                  // G_64 per key channel
+};
+struct ChunkPrep {
+    uint16_t T[2][kTri][kFrag];
+    uint16_t P[2][kTri][kFrag];
+    ChunkMeta m;
+};
+static_assert(sizeof(ChunkPrep) % 256 == 0, "entries of the workspace stay aligned");
+
+struct ChunkArgs {
+    SeqArgs s;
+    const float *initial;            // [B,H,d_k,d_v] or nullptr
+    float *last;                     // [B,H,d_k,d_v] or nullptr
+    void *o;                         // [N,H,d_v] io dtype
+    ChunkPrep *prep;                 // [chunk slots][H]
+    int32_t slots;                   // chunk slots: N / 64 + B
+};
+
+// Chunk c of sequence b (first token t0) has slot t0 / 64 + b + c: slots of
+// different chunks differ, and none reaches N / 64 + B.
+inline int chunk_slots(int N, int B) { return N / kC + B; }
+
+hipError_t launch_chunk_prep(const ChunkArgs &a, int dk, bool keyvec, bool bf16, hipStream_t s);
+hipError_t launch_chunk_forward(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);
+
+#if defined(__HIPCC__)
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+// The chunk of slot x: its sequence, first token and number of tokens; 0 tokens
+// where the slot holds none.
+__device__ inline int chunk_of_slot(const SeqArgs &s, int x, int &b, int &first) {
+    int lo = 0, hi = s.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (min(max(s.cu[mid], 0), s.N) / kC + mid <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo;
+    int t0, t1;
+    seq_range(s, b, t0, t1);
+    const int c = x - (t0 / kC + b);
+    first = t0 + c * kC;
+    return c < 0 ? 0 : min(max(t1 - first, 0), kC);
+}
+
+// 2^(top - floor(log2 m)) and its inverse, for m >= 0 (tiny m: as for 2^(top - 112)).
+__device__ inline float scale_to(float m, int top, float &inv) {
+    const int e = max((int)(__float_as_uint(m) >> 23) & 255, top + 1);
+    inv = __uint_as_float((uint32_t)(e - top) << 23);
+    return __uint_as_float((uint32_t)(254 + top - e) << 23);
+}
+
+__device__ inline floatx4 mfma16(half8 a, half8 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ inline floatx4 mfma_f32(float a, float b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// x s as hi + lo
+__device__ inline void split(float x, float s, _Float16 &hi, _Float16 &lo) {
+    hi = (_Float16)(x * s);
+    lo = (_Float16)__builtin_fmaf(x, s, -(float)hi);
+}
+
+// max over the lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ inline float max_groups(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// Index of fragment (row tile, k step) of a lower triangular matrix.
+__device__ constexpr int tri(int rt, int ks) { return rt < 2 ? rt : 2 + 2 * (rt - 2) + ks; }
+
+#endif  // __HIPCC__
+
+}  // namespace stq

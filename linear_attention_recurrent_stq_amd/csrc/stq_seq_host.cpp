@@ -6,7 +6,7 @@
 
 #include "stq.h"
 
-#include "stq_seq.h"
+#include "stq_chunk.h"
 
 namespace stq {
 void set_error(const std::string &msg);  // stq_host.cpp
@@ -115,6 +115,47 @@ stq_status stq_recurrent_step(const stq_rule *rule, int32_t B, int32_t N, const 
     return launched(stq::launch_recurrent(a, rule->d_k, rule->d_v, rule->gate == STQ_GATE_KEYVEC,
                                           rule->io_dtype == STQ_BF16, static_cast<hipStream_t>(stream)),
                     "recurrent step");
+}
+
+stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32_t backward,
+                               size_t *bytes) {
+    stq::set_error("");
+    if (stq_status s = check_rule(rule)) return s;
+    if (stq_status s = check_sizes(rule, B, N)) return s;
+    if (!bytes) return fail(STQ_ERR_INVALID, "bytes is NULL");
+    if (backward) return fail(STQ_ERR_UNSUPPORTED, "no backward pass");
+    *bytes = sizeof(stq::ChunkPrep) * (size_t)stq::chunk_slots(N, B) * rule->H;
+    return STQ_OK;
+}
+
+stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
+                             const void *d_q, const void *d_k, const void *d_v, const float *d_a,
+                             const float *d_beta, const float *d_initial, void *d_o, float *d_final,
+                             void *d_workspace, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    if (stq_status s = stq_chunk_workspace(rule, B, N, 0, &need)) return s;
+    if (B > 65535) return fail(STQ_ERR_UNSUPPORTED, "B exceeds 65535");
+    if (B == 0) return STQ_OK;
+    if (stq_status s = check_ints(d_cu_seqlens, true, "cu_seqlens")) return s;
+    if (N > 0)  // without tokens the states are passed on and nothing else is touched
+        if (stq_status s = check_ptrs({d_q, d_k, d_v, d_a, d_beta, d_o})) return s;
+    if (stq_status s = check_ptrs({d_workspace})) return s;
+    if (!aligned(d_initial, 16) || !aligned(d_final, 16))
+        return fail(STQ_ERR_ALIGN, "states must be 16-byte aligned");
+    if (workspace_bytes < need) return fail(STQ_ERR_TOO_SMALL, "workspace smaller than stq_chunk_workspace");
+    stq::ChunkArgs a{};
+    a.s = seq_args(rule, B, N, d_cu_seqlens, d_q, d_k, d_v, d_a, d_beta);
+    a.initial = d_initial;
+    a.last = d_final;
+    a.o = d_o;
+    a.prep = static_cast<stq::ChunkPrep *>(d_workspace);
+    a.slots = stq::chunk_slots(N, B);
+    const bool keyvec = rule->gate == STQ_GATE_KEYVEC, bf16 = rule->io_dtype == STQ_BF16;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (N > 0)
+        if (stq_status s = launched(stq::launch_chunk_prep(a, rule->d_k, keyvec, bf16, st), "chunk preparation"))
+            return s;
+    return launched(stq::launch_chunk_forward(a, rule->d_k, rule->d_v, keyvec, bf16, st), "chunk forward");
 }
 
 stq_status stq_verify_workspace(int32_t B, int32_t V, size_t *bytes) {

@@ -46,6 +46,11 @@ def _rel(got, want):
     return np.linalg.norm(np.asarray(got, np.float64) - want) / n if n else np.abs(got).max()
 
 
+def _within(got, want, tol):
+    r = float(_rel(got, want))
+    assert r < tol
+
+
 # ---------------------------------------------------------------- recurrent
 # A token's sums have d_k / 8 terms in a lane and three cross-lane adds, then
 # four more roundings: an error of at most (d_k / 8 + 7) E32 of the state's and
@@ -79,8 +84,8 @@ def test_recurrent(stq, dk, dv, keyvec, bf16):
         want[ids] = last if given is None else kept
         go, gS = o.cpu().numpy(), S.cpu().numpy()
         assert (go[at[-1]:] == 7).all()
-        assert _rel(go[:at[-1]], wo[:at[-1]]) < _step_tol(dk, max(lens))
-        assert _rel(gS, want) < _step_tol(dk, max(lens))
+        _within(go[:at[-1]], wo[:at[-1]], _step_tol(dk, max(lens)))
+        _within(gS, want, _step_tol(dk, max(lens)))
         for s in range(slots):           # untouched slots keep their bits
             if s not in ids or lens[list(ids).index(s)] == 0 or (given is not None and s == 3):
                 assert np.array_equal(gS[s], S0[s]), s
@@ -108,7 +113,7 @@ def test_recurrent_equals_single_tokens_and_decode(stq):
         stq.recurrent_step(S1, ids, cu1, z["q"], z["k"], z["v"], z["a"], z["beta"], one)
         assert torch.equal(one, o.view(B, T, H, d)[:, t])
         stq.decode_step(pool, ids, z["q"], z["k"], z["v"], z["a"], z["beta"], od)
-        assert _rel(od.cpu().numpy(), one.double().cpu().numpy()) < 2 * _step_tol(d, T)
+        _within(od.cpu().numpy(), one.double().cpu().numpy(), 2 * _step_tol(d, T))
     assert torch.equal(S, S1)
 
 
@@ -150,6 +155,216 @@ def test_recurrent_python_refusals(stq):
         with pytest.raises((ValueError, stq.StqError)):
             stq.recurrent_step(**{**good, **bad})
     stq.recurrent_step(**good)
+
+
+# ------------------------------------------------------------------ chunks
+# Errors of the chunked form, relative to the norm of the result.  A chunk's
+# matrix products take operands of 22 bits, relative to the largest value of
+# their row or column (which is up to sqrt(128) of its root mean square: 3.5
+# bits), and sum 128 of them in fp32 in an order that the matrix units choose
+# (at most 128 E32, in practice its root).  Six products stand one behind another,
+# and the state passes through the chunks without enlarging an error (|k| <= 1,
+# beta <= 1, a <= 1), a chunk's own errors adding to it.  So a result is within
+# chunks * 6 * (2^-22 * 2^3.5 + 128 E32) of its norm; the outputs are then
+# rounded to their type.
+def _chunk_tol(lens):
+    chunks = max(1, -(-max(lens) // 64))
+    return chunks * 6 * (2.0 ** -18.5 + 128 * E32)
+
+
+def _io_step(bf16):
+    return 2.0 ** -8 if bf16 else E32
+
+
+LENS = {"one": [1], "short": [3, 0, 17, 64, 1], "edge": [63, 65, 128, 127, 129, 0], "long": [500, 31]}
+
+
+@pytest.mark.parametrize("lens", list(LENS))
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("keyvec,bf16", [(False, False), (False, True), (True, False), (True, True)])
+def test_chunk_forward(stq, lens, dk, dv, keyvec, bf16):
+    rng = np.random.default_rng(dk + 2 * dv)
+    lens, H = LENS[lens], 2
+    at, cu = _cu(lens)
+    n, B = at[-1] + 2, len(lens)         # two tokens behind the last sequence
+    x, y = _inputs(rng, n, H, dk, dv, keyvec, bf16)
+    S0 = rng.normal(size=(B, H, dk, dv)).astype(np.float32)
+    S = torch.from_numpy(S0).cuda()
+    plan = stq.ChunkPlan(H, dk, dv, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32, max_tokens=n + 70,
+                         max_seqs=B + 1)
+    plan.workspace.fill_(255)            # what the workspace held does not matter
+    o = torch.full_like(x["v"], 7.0)
+    last = torch.full_like(S, 7.0)
+    ins = (cu, x["q"], x["k"], x["v"], x["a"], x["beta"])
+    stq.chunk_forward(plan, *ins, o, initial_state=S, final_state=last)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), S0)
+    go = o.double().cpu().numpy()
+    assert (go[at[-1]:] == 7).all()
+    _within(go[:at[-1]], wo[:at[-1]], _chunk_tol(lens) + _io_step(bf16))
+    _within(last.cpu().numpy(), wl, _chunk_tol(lens))
+    for b in range(B):                   # sequence by sequence: a small one is not lost in a large one
+        _within(last[b].cpu().numpy(), wl[b], _chunk_tol(lens))
+        if lens[b] == 0:
+            assert torch.equal(last[b], S[b])
+    # in place, the same bits; without states, from zero
+    o2 = torch.zeros_like(o)
+    stq.chunk_forward(plan, *ins, o2, initial_state=S, final_state=S)
+    assert torch.equal(o2[:at[-1]], o[:at[-1]]) and torch.equal(S, last)
+    stq.chunk_forward(plan, *ins, o2)
+    wo, _, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), np.zeros_like(S0))
+    _within(o2.double().cpu().numpy()[:at[-1]], wo[:at[-1]], _chunk_tol(lens) + _io_step(bf16))
+
+
+@pytest.mark.parametrize("keyvec,bf16", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("what", ["resets", "strong", "beta0", "tiny", "large", "same keys", "zero"])
+def test_chunk_forward_extremes(stq, keyvec, bf16, what):
+    """Gates of 0 and gates that underflow over a chunk, write strengths of 0
+    and 1, values and states of extreme size, keys that are all the same, and
+    all zeros."""
+    rng = np.random.default_rng(11)
+    lens, H, d = [150, 64], 3, 128
+    at, cu = _cu(lens)
+    n = at[-1]
+    x, y = _inputs(rng, n, H, d, d, keyvec, bf16)
+    S0 = rng.normal(size=(2, H, d, d)).astype(np.float32)
+    if what == "resets":
+        x["a"][::7] = 0.0
+    elif what == "strong":
+        x["a"].mul_(1e-3)
+        x["a"][:, 1] = 1.0
+        x["a"][5:9] = 1e-30
+    elif what == "beta0":
+        x["beta"][::2] = 0.0
+        x["beta"][1::4] = 1.0
+        x["beta"][3] = 1e-20
+    elif what == "tiny":
+        for m in ("v", "q"):
+            x[m].mul_(2.0 ** -60)
+        x["k"][::3].mul_(2.0 ** -40)
+        S0 *= np.float32(2.0 ** -60)
+    elif what == "large":
+        x["v"].mul_(2.0 ** 60)
+        x["q"].mul_(2.0 ** 30)
+        x["v"][:, :, 3].mul_(2.0 ** -50)
+        S0 *= np.float32(2.0 ** 60)
+    elif what == "same keys":
+        x["k"][:] = x["k"][0]
+    else:
+        for m in ("q", "k", "v", "beta"):
+            x[m].zero_()
+        S0[:] = 0
+    y = {m: t.double().cpu().numpy() for m, t in x.items()}
+    S = torch.from_numpy(S0).cuda()
+    plan = stq.ChunkPlan(H, d, d, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32, max_tokens=n, max_seqs=2)
+    o, last = torch.empty_like(x["v"]), torch.empty_like(S)
+    stq.chunk_forward(plan, cu, x["q"], x["k"], x["v"], x["a"], x["beta"], o, initial_state=S, final_state=last)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), S0)
+    _within(o.double().cpu().numpy(), wo, _chunk_tol(lens) + _io_step(bf16))
+    _within(last.cpu().numpy(), wl, _chunk_tol(lens))
+    if what == "large":                  # a small column keeps its own accuracy
+        _within(o.double().cpu().numpy()[:, :, 3], wo[:, :, 3], _chunk_tol(lens) + _io_step(bf16))
+
+
+def test_chunk_forward_sequences_apart(stq):
+    """A NaN or infinity in one sequence and head stays there; a sequence gives the
+    same bits alone and in a batch; a bad table of starts writes nothing outside."""
+    rng = np.random.default_rng(2)
+    lens, H, d = [100, 70, 1], 2, 128
+    at, cu = _cu(lens)
+    x, _ = _inputs(rng, at[-1], H, d, d, True, True)
+    ins = [x[m] for m in ("q", "k", "v", "a", "beta")]
+    plan = stq.ChunkPlan(H, d, d, gate=1, max_tokens=at[-1], max_seqs=3)
+    o, last = torch.empty_like(x["v"]), torch.empty(3, H, d, d, device="cuda")
+    stq.chunk_forward(plan, cu, *ins, o, final_state=last)
+    x["v"][at[1] + 3, 0, 5] = float("nan")
+    x["k"][at[1] + 9, 0, 5] = float("inf")
+    o2, last2 = torch.empty_like(o), torch.empty_like(last)
+    stq.chunk_forward(plan, cu, *ins, o2, final_state=last2)
+    assert torch.isnan(last2[1, 0]).any()
+    for t, t2 in ((o, o2), (last, last2)):
+        lo, hi = (at[1], at[2]) if t is o else (1, 2)
+        assert torch.equal(t[:lo], t2[:lo]) and torch.equal(t[hi:], t2[hi:]) and torch.equal(t[lo:hi, 1], t2[lo:hi, 1])
+    one = torch.empty_like(o)[:lens[0]]
+    l1 = torch.empty(1, H, d, d, device="cuda")
+    stq.chunk_forward(plan, cu[:2], *[t[:lens[0]] for t in ins], one, final_state=l1)
+    assert torch.equal(one, o[:lens[0]]) and torch.equal(l1[0], last[0])
+    guard = torch.full((at[-1] + 64, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    for bad in ([-5, 400, 20, 90], [171, 0, 171, 0], [3, 2, 1, 0]):
+        stq.chunk_forward(plan, _dev(np.array(bad, np.int32), torch.int32), *ins, guard[:at[-1]], final_state=last2)
+        assert (guard[at[-1]:] == 7).all()
+
+
+def test_chunk_forward_then_steps(stq):
+    """The pieces together: a prompt by chunks, its last tokens one by one from
+    the state it left, against the whole sequence at once."""
+    rng = np.random.default_rng(8)
+    H, d, B, n = 4, 128, 3, 140
+    at, cu = _cu([n] * B)
+    x, y = _inputs(rng, B * n, H, d, d, False, True)
+    v = {m: x[m].view(B, n, *x[m].shape[1:]) for m in x}
+    plan = stq.ChunkPlan(H, d, d, max_tokens=B * n, max_seqs=B)
+    cut = 133
+    head = [v[m][:, :cut].reshape(B * cut, *x[m].shape[1:]).contiguous() for m in ("q", "k", "v", "a", "beta")]
+    tail = [v[m][:, cut:].reshape(B * (n - cut), *x[m].shape[1:]).contiguous() for m in ("q", "k", "v", "a", "beta")]
+    S = torch.empty(B, H, d, d, device="cuda")
+    o1 = torch.empty_like(head[2])
+    stq.chunk_forward(plan, _cu([cut] * B)[1], *head, o1, final_state=S)
+    o2 = torch.empty(B * (n - cut), H, d, device="cuda")
+    stq.recurrent_step(S, None, _cu([n - cut] * B)[1], *tail, o2)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), np.zeros((B, H, d, d)))
+    wo = wo.reshape(B, n, H, d)
+    tol = _chunk_tol([n]) + _step_tol(d, n - cut)
+    _within(o2.cpu().numpy().reshape(B, n - cut, H, d), wo[:, cut:], tol)
+    _within(S.cpu().numpy(), wl, tol)
+    _within(o1.double().cpu().numpy().reshape(B, cut, H, d), wo[:, :cut], tol + 2.0 ** -8)
+
+
+def test_chunk_forward_in_a_graph(stq):
+    """Captured once, replayed on new inputs in place, with eager work between."""
+    rng = np.random.default_rng(4)
+    lens, H, d = [90, 64, 5], 2, 64
+    at, cu = _cu(lens)
+    plan = stq.ChunkPlan(H, d, d, gate=1, max_tokens=at[-1], max_seqs=3)
+    other = stq.ChunkPlan(H, d, d, gate=1, max_tokens=at[-1], max_seqs=3)
+    x, _ = _inputs(rng, at[-1], H, d, d, True, True)
+    names = ("q", "k", "v", "a", "beta")
+    o, S = torch.empty_like(x["v"]), torch.zeros(3, H, d, d, device="cuda")
+    o2, S2 = torch.empty_like(o), torch.empty_like(S)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        stq.chunk_forward(plan, cu, *[x[m] for m in names], o, initial_state=S, final_state=S)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stq.chunk_forward(plan, cu, *[x[m] for m in names], o, initial_state=S, final_state=S)
+    for i in range(4):
+        new, _ = _inputs(rng, at[-1], H, d, d, True, True)
+        for m in names:
+            x[m].copy_(new[m])
+        S2.copy_(S)
+        stq.chunk_forward(other, cu, *[new[m] for m in names], o2, initial_state=S2, final_state=S2)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+def test_chunk_python_refusals(stq):
+    H, d, n = 2, 64, 5
+    x, _ = _inputs(np.random.default_rng(0), n, H, d, d, False, True)
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    plan = stq.ChunkPlan(H, d, d, max_tokens=n, max_seqs=2)
+    S = torch.zeros(2, H, d, d, device="cuda")
+    good = dict(plan=plan, cu_seqlens=cu, o=torch.empty_like(x["v"]), initial_state=S, final_state=S, **x)
+    more = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in (dict(cu_seqlens=more), dict(cu_seqlens=cu.long()), dict(o=good["o"].float()), dict(o=good["o"][:3]),
+                dict(initial_state=S[:1]), dict(final_state=S.double()), dict(a=x["a"][:, :, None].expand(n, H, d)),
+                dict(q=x["q"].float(), k=x["k"].float(), v=x["v"].float()), dict(k=x["k"][:, :1]),
+                dict(plan=stq.ChunkPlan(H, d, d, max_tokens=4, max_seqs=2)),
+                dict(plan=stq.ChunkPlan(H, d, 128, max_tokens=n, max_seqs=2))):
+        with pytest.raises((ValueError, stq.StqError)):
+            stq.chunk_forward(**{**good, **bad})
+    stq.chunk_forward(**good)
 
 
 # ------------------------------------------------------------------- verify
