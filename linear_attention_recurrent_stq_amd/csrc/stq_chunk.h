@@ -45,12 +45,19 @@ struct ChunkPrep {
 };
 static_assert(sizeof(ChunkPrep) % 256 == 0, "entries of the workspace stay aligned");
 
+// Key-vector gates: per channel, the products of the gates before and after each
+// four tokens of a chunk.
+struct ChunkGates {
+    float pre[kC / 4][128], suf[kC / 4][128];
+};
+
 struct ChunkArgs {
     SeqArgs s;
     const float *initial;            // [B,H,d_k,d_v] or nullptr
     float *last;                     // [B,H,d_k,d_v] or nullptr
     void *o;                         // [N,H,d_v] io dtype
     ChunkPrep *prep;                 // [chunk slots][H]
+    ChunkGates *gates;               // the same, key-vector gates only
     int32_t slots;                   // chunk slots: N / 64 + B
 };
 
@@ -105,10 +112,42 @@ __device__ inline void split(float x, float s, _Float16 &hi, _Float16 &lo) {
     lo = (_Float16)__builtin_fmaf(x, s, -(float)hi);
 }
 
-// max over the lanes l, l ^ 16, l ^ 32, l ^ 48
+// Lanes l and l ^ 16, or l ^ 32, exchanged by one vector instruction: both of a pair get
+// both values.
 __device__ inline float max_groups(float x) {
-    x = fmaxf(x, __shfl_xor(x, 16));
-    return fmaxf(x, __shfl_xor(x, 32));
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// x[j] of lane i of a quad becomes x[i] of lane j.
+template <int ctrl>
+__device__ inline float quad_swap(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), ctrl, 0xf, 0xf, true));
+}
+__device__ inline void quad_transpose(float (&x)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+    for (int p = 0; p < 4; p += 2) {
+        const float r = quad_swap<0xB1>(odd ? x[p] : x[p + 1]);
+        x[p] = odd ? r : x[p];
+        x[p + 1] = odd ? x[p + 1] : r;
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float r = quad_swap<0x4E>(high ? x[p] : x[p + 2]);
+        x[p] = high ? r : x[p];
+        x[p + 2] = high ? x[p + 2] : r;
+    }
+}
+
+// A workgroup barrier for values in LDS: it waits for this wave's LDS accesses, not for
+// its loads from memory, which stay in flight.
+__device__ inline void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Index of fragment (row tile, k step) of a lower triangular matrix.

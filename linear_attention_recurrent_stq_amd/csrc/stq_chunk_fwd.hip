@@ -3,49 +3,57 @@
 // Per chunk, from T, P and the factors that k_chunk_prep left (stq_chunk.h):
 //   R = V - (K G) S;   u = T R;   O = (Q G) S + P u;   S = diag(G_64) S + (K G_64/G)^T u.
 //
-// Columns of S are independent, so each of four waves owns 16 NT of them for
-// the whole sequence: S stays in its registers, and no wave waits for another's
-// values.  A result tile of the matrix instructions holds column l % 16 in lane
-// l, which is where a right operand wants it, so S, R and u go from one product
-// into the next without leaving the registers; only the order of a left
-// operand's columns is permuted to match (4 g + e and 16 + 4 g + e in lane group
-// g).  The left operands K, Q, K^T, T and P are the same for every wave: four
-// more waves turn the next chunk's rows into scaled fp16 fragments in LDS
-// while the first four multiply.
+// Columns of S are independent, so a wave owns 16 of them for the whole
+// sequence: S stays in its registers, and no wave waits for another's values.
+// A result tile of the matrix instructions holds column l % 16 in lane l, which
+// is where a right operand wants it, so S, R and u go from one product into the
+// next without leaving the registers; only the order of a left operand's columns
+// is permuted to match (4 g + e and 16 + 4 g + e in lane group g).
 //
-// Scalar bf16 rules need no lo parts of K and Q (exact in fp16) and fit two
-// chunks of fragments in LDS: one barrier a chunk.  The others fold G into K and
-// Q (key-vector gates) or carry fp32 rows, as hi + lo: one chunk fits, and the
-// write of the next one stands between two barriers.
+// The left operands K, Q, T, P and K^T are the same for every wave.  Four
+// producing waves turn the next chunk's rows into scaled fp16 fragments in LDS
+// while the others multiply.  The fragments need no second buffer: K and Q are
+// read in the first half of a chunk, T, P and K^T in the second, and each half's are
+// replaced while the other half runs (two barriers a chunk, which wait for
+// LDS only).
 //
-// NT = 2 (a workgroup takes 128 columns) halves the fragments read from LDS per
-// matrix instruction; NT = 1 halves the time of a chunk and is taken when there
-// are too few (sequence, head) pairs to fill the chip.
+// Eight multiplying waves take the 128 columns of a (sequence, head), so that
+// two share a SIMD and fill each other's waits; with fewer pairs than compute
+// units, two workgroups of four waves take 64 each.
+//
+// v and o are read and written four columns of a row a lane, and turned within
+// quads of lanes.
 #include "stq_chunk.h"
 
 namespace stq {
 namespace {
 
-constexpr int kMeta = sizeof(ChunkMeta) / 16;  // 16-byte pieces
-constexpr int kTP = 2 * 2 * kTri * kFrag * 2 / 16;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-template <int DK, bool LO>
+constexpr int kMeta = sizeof(ChunkMeta) / 16;  // 16-byte pieces
+constexpr int kPart = kTri * kFrag * 2 / 16;   // of T's or P's hi or lo part
+
+// What a rule's operands carry.  K and T, which the state depends on, always
+// keep 22 bits: K in its hi part alone where it is bf16 and not folded with gates.  Q
+// and P reach the outputs only; for bf16 outputs (half a step: 2^-9) their hi
+// parts, and those of what they multiply, are enough (2^-12).
+template <int DK, bool KEYVEC, bool BF16>
 struct FwdShared {
-    static constexpr int NL = LO ? 2 : 1, NBUF = LO ? 1 : 2, KS = DK / 32, CT = DK / 16;
-    struct Buf {
-        _Float16 K[NL][4][KS][kFrag], Q[NL][4][KS][kFrag], W[NL][CT][2][kFrag];
-        uint4 TP[kTP];               // T hi, T lo, P hi, P lo
-        ChunkMeta m;
-    } buf[NBUF];
-    float gp[LO ? 16 : 1][DK];       // gate products of four tokens
+    static constexpr int NK = KEYVEC || !BF16 ? 2 : 1, NQ = BF16 ? 1 : 2, KS = DK / 32, CT = DK / 16;
+    static constexpr int TP = (2 + NQ) * kPart;  // 16-byte pieces of T hi, T lo, P hi (, P lo)
+    _Float16 K[NK][4][KS][kFrag], Q[NQ][4][KS][kFrag];
+    u32x4 tp[TP];
+    ChunkMeta m[2];                  // of even and of odd chunks
+    _Float16 W[NK][CT][2][kFrag];
 };
 
 // Where lane (row, g)'s eight halves stand in a fragment: rows are permuted so
-// that the producers' writes (fixed row, all g and k steps) and the consumers'
-// reads (fixed k step, all rows) both spread over the banks.
+// that the producers' writes (fixed row, all g and k steps) and the readers'
+// (fixed k step, all rows) both spread over the banks.
 __device__ inline int place_k(int row16, int g, int ks) { return (g * 16 + (row16 ^ ((4 * g + ks) & 15))) * 8; }
 __device__ inline int place_w(int ch16, int g, int ct) { return (g * 16 + (ch16 ^ (ct & 3))) * 8; }
 
+// Four elements as they are in memory.
 template <bool BF16> struct Raw4;
 template <> struct Raw4<true> { typedef uint2 type; };
 template <> struct Raw4<false> { typedef float4 type; };
@@ -62,92 +70,106 @@ __device__ inline void widen(float4 w, float (&x)[4]) {
     x[2] = w.z;
     x[3] = w.w;
 }
+__device__ inline void narrow(const float (&x)[4], uint2 &w) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union { bf16x2 v; uint32_t u; } a, b;
+    a.v = bf16x2{(__bf16)x[0], (__bf16)x[1]};
+    b.v = bf16x2{(__bf16)x[2], (__bf16)x[3]};
+    w = make_uint2(a.u, b.u);
+}
+__device__ inline void narrow(const float (&x)[4], float4 &w) { w = make_float4(x[0], x[1], x[2], x[3]); }
 
-// The producing waves: 256 threads; a unit is 4 tokens x 4 channels.
+// The producing waves; a unit is 4 tokens x 4 channels.  Rules with lo parts of
+// K take a thread a unit (with two, the raw rows and the K^T kept back spill).
 template <int DK, bool KEYVEC, bool BF16>
 struct Producer {
-    static constexpr bool LO = KEYVEC || !BF16;
-    static constexpr int CG = DK / 4, U = DK / 64;  // channel groups; units of a thread
+    typedef FwdShared<DK, KEYVEC, BF16> Shared;
     typedef typename Raw4<BF16>::type raw;
-    typedef FwdShared<DK, LO> Shared;
+    static constexpr int NK = Shared::NK, NQ = Shared::NQ;
+    static constexpr int PT = NK == 2 ? 4 * DK : 256;        // producing threads
+    static constexpr int CG = DK / 4, U = 4 * DK / PT;       // channel groups; units of a thread
     raw k[U][4], q[U][4];
-    float4 a[KEYVEC ? U : 1][4];
-    uint4 tp[kTP / 256], meta;
-    float sk[U][4], sq[U][4];
+    float4 a[KEYVEC ? U : 1][4], pre[KEYVEC ? U : 1], suf[KEYVEC ? U : 1], sk[U], sq[U];
+    u32x4 tp0, tp1, tp2, tp3, tp4, tp5, meta;
+    half4 w[U][NK][4];               // K^T fragments of the chunk whose K and Q are written
+    int n;                           // tokens of the chunk in k, q and a
 
-    __device__ inline void load(const ChunkArgs &A, int h, int first, int n, const ChunkPrep *e, int tid) {
+    __device__ static inline int channels(int u, int tid) { return (tid + PT * u) % CG; }
+    __device__ static inline int tokens(int u, int tid) { return (tid + PT * u) / CG; }
+
+    __device__ inline void load(const ChunkArgs &A, int h, int first, int n_, size_t entry, int tid) {
+        n = n_;
+        const ChunkPrep *e = A.prep + entry;
+        const size_t base = ((size_t)first * A.s.H + h) * CG;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int cg = (tid + 256 * u) % CG, tg = (tid + 256 * u) / CG;
+            const int cg = channels(u, tid), tg = tokens(u, tid);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 4 * tg + i;
-                k[u][i] = q[u][i] = raw{};
-                if constexpr (KEYVEC) a[u][i] = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (t < n) {
-                    const size_t at = (((size_t)(first + t) * A.s.H + h) * DK) / 4 + cg;
-                    k[u][i] = static_cast<const raw *>(A.s.k)[at];
-                    q[u][i] = static_cast<const raw *>(A.s.q)[at];
-                    if constexpr (KEYVEC) a[u][i] = reinterpret_cast<const float4 *>(A.s.a)[at];
-                }
-                sk[u][i] = e->m.sk[t];
-                sq[u][i] = e->m.sq[t];
+                // past the last token its row again: T has zeros in those columns and rows,
+                // so whatever finite values stand there add nothing
+                const uint32_t at = (uint32_t)min(4 * tg + i, n - 1) * (uint32_t)(A.s.H * CG) + cg;
+                k[u][i] = (static_cast<const raw *>(A.s.k) + base)[at];
+                q[u][i] = (static_cast<const raw *>(A.s.q) + base)[at];
+                if constexpr (KEYVEC) a[u][i] = (reinterpret_cast<const float4 *>(A.s.a) + base)[at];
             }
+            if constexpr (KEYVEC) {
+                pre[u] = *reinterpret_cast<const float4 *>(&A.gates[entry].pre[tg][4 * cg]);
+                suf[u] = *reinterpret_cast<const float4 *>(&A.gates[entry].suf[tg][4 * cg]);
+            }
+            sk[u] = *reinterpret_cast<const float4 *>(&e->m.sk[4 * tg]);
+            sq[u] = *reinterpret_cast<const float4 *>(&e->m.sq[4 * tg]);
         }
-        const uint4 *src = reinterpret_cast<const uint4 *>(e);
-#pragma unroll
-        for (int i = 0; i < kTP / 256; ++i) tp[i] = src[tid + 256 * i];
-        if (tid < kMeta) meta = src[kTP + tid];
+        if (tid < kMeta) meta = reinterpret_cast<const u32x4 *>(&e->m)[tid];
     }
 
-    // Key-vector gates: the product of the unit's four gates per channel.
-    __device__ inline void groups(Shared &sh, int tid) {
-        if constexpr (KEYVEC) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int cg = (tid + 256 * u) % CG, tg = (tid + 256 * u) / CG;
-                float4 p = a[u][0];
-#pragma unroll
-                for (int i = 1; i < 4; ++i) {
-                    p.x *= a[u][i].x;
-                    p.y *= a[u][i].y;
-                    p.z *= a[u][i].z;
-                    p.w *= a[u][i].w;
-                }
-                *reinterpret_cast<float4 *>(&sh.gp[tg][4 * cg]) = p;
-            }
-        }
+    // f(piece, its number) over this thread's pieces of T and P
+    template <class F>
+    __device__ inline void pieces(int tid, F f) {
+        constexpr int TP = Shared::TP;
+        f(tp0, tid);
+        f(tp1, tid + PT);
+        if (2 * PT + PT <= TP || tid + 2 * PT < TP) f(tp2, tid + 2 * PT);
+        if constexpr (3 * PT < TP) f(tp3, tid + 3 * PT);
+        if constexpr (4 * PT < TP)
+            if (5 * PT <= TP || tid + 4 * PT < TP) f(tp4, tid + 4 * PT);
+        if constexpr (5 * PT < TP) f(tp5, tid + 5 * PT);
     }
 
-    __device__ inline void write(Shared &sh, int which, int tid) {
-        auto &B = sh.buf[which];
+    __device__ inline void load_tp(const ChunkPrep *e, int tid) {
+        pieces(tid, [&](u32x4 &x, int i) { x = reinterpret_cast<const u32x4 *>(e)[i]; });
+    }
+
+    // Gate of token t in a unit's channels: 1 past the last token.
+    __device__ inline void gate(int u, int i, int t, float (&x)[4]) const {
+        widen(a[u][i], x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = t < n ? x[c] : 1.f;
+    }
+
+    // K and Q of the chunk into LDS, its K^T into w.
+    __device__ inline void write_kq(Shared &sh, int which, int tid) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int cg = (tid + 256 * u) % CG, tg = (tid + 256 * u) / CG;
-            float pre[4] = {1.f, 1.f, 1.f, 1.f}, suf[4][4];
+            const int cg = channels(u, tid), tg = tokens(u, tid);
+            float before[4], after[4][4];  // gate products up to and past a token
             if constexpr (KEYVEC) {
-                float s[4] = {1.f, 1.f, 1.f, 1.f};
-                for (int m = 0; m < 16; ++m) {
-                    const float4 p = *reinterpret_cast<const float4 *>(&sh.gp[m][4 * cg]);
-                    const float x[4] = {p.x, p.y, p.z, p.w};
+                widen(pre[u], before);
+                float s[4];
+                widen(suf[u], s);
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    float x[4];
+                    gate(u, i, 4 * tg + i, x);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        pre[c] *= m < tg ? x[c] : 1.f;
-                        s[c] *= m > tg ? x[c] : 1.f;
+                        after[i][c] = s[c];
+                        s[c] *= x[c];
                     }
-                }
-#pragma unroll
-                for (int i = 3; i >= 0; --i) {  // products of the gates after token i
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) suf[i][c] = s[c];
-                    float x[4];
-                    widen(a[u][i], x);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[c] *= x[c];
                 }
             }
             const int g = cg & 3, ks = cg >> 3, eh = ((cg >> 2) & 1) * 4, rt = tg >> 2;
-            _Float16 wh[4][4], wl[4][4];
+            const float ek[4] = {sk[u].x, sk[u].y, sk[u].z, sk[u].w}, eq[4] = {sq[u].x, sq[u].y, sq[u].z, sq[u].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float kx[4], qx[4];
@@ -155,59 +177,71 @@ struct Producer {
                 widen(q[u][i], qx);
                 if constexpr (KEYVEC) {
                     float x[4];
-                    widen(a[u][i], x);
+                    gate(u, i, 4 * tg + i, x);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) pre[c] *= x[c];
+                    for (int c = 0; c < 4; ++c) before[c] *= x[c];
                 }
                 half4 kh, kl, qh, ql;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     _Float16 hi, lo;
-                    if constexpr (LO) {
-                        split(KEYVEC ? kx[c] * pre[c] : kx[c], sk[u][i], hi, lo);
+                    if constexpr (NK == 2) {
+                        split(KEYVEC ? kx[c] * before[c] : kx[c], ek[i], hi, lo);
                         kh[c] = hi;
                         kl[c] = lo;
-                        if constexpr (KEYVEC) split(kx[c] * suf[i][c], sk[u][i], hi, lo);
-                        wh[i][c] = hi;
-                        wl[i][c] = lo;
-                        split(KEYVEC ? qx[c] * pre[c] : qx[c], sq[u][i], hi, lo);
-                        qh[c] = hi;
-                        ql[c] = lo;
+                        if constexpr (KEYVEC) split(kx[c] * after[i][c], ek[i], hi, lo);
+                        w[u][0][c][i] = hi;
+                        w[u][NK - 1][c][i] = lo;
                     } else {
-                        kh[c] = wh[i][c] = (_Float16)(kx[c] * sk[u][i]);
-                        qh[c] = (_Float16)(qx[c] * sq[u][i]);
+                        kh[c] = w[u][0][c][i] = (_Float16)(kx[c] * ek[i]);
                     }
+                    split(KEYVEC ? qx[c] * before[c] : qx[c], eq[i], hi, lo);
+                    qh[c] = hi;
+                    ql[c] = lo;
                 }
                 const int at = place_k(4 * (tg & 3) + i, g, ks) + eh;
-                *reinterpret_cast<half4 *>(&B.K[0][rt][ks][at]) = kh;
-                *reinterpret_cast<half4 *>(&B.Q[0][rt][ks][at]) = qh;
-                if constexpr (LO) {
-                    *reinterpret_cast<half4 *>(&B.K[1][rt][ks][at]) = kl;
-                    *reinterpret_cast<half4 *>(&B.Q[1][rt][ks][at]) = ql;
-                }
+                *reinterpret_cast<half4 *>(&sh.K[0][rt][ks][at]) = kh;
+                *reinterpret_cast<half4 *>(&sh.Q[0][rt][ks][at]) = qh;
+                if constexpr (NK == 2) *reinterpret_cast<half4 *>(&sh.K[NK - 1][rt][ks][at]) = kl;
+                if constexpr (NQ == 2) *reinterpret_cast<half4 *>(&sh.Q[NQ - 1][rt][ks][at]) = ql;
             }
+        }
+        if (tid < kMeta) reinterpret_cast<u32x4 *>(&sh.m[which])[tid] = meta;
+    }
+
+    __device__ inline void write_tpw(Shared &sh, int tid) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int cg = channels(u, tid), tg = tokens(u, tid);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int ch = 4 * cg + c, ct = ch >> 4;
                 const int at = place_w(ch & 15, tg & 3, ct) + ((tg >> 2) & 1) * 4;
-                half4 w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = wh[i][c];
-                *reinterpret_cast<half4 *>(&B.W[0][ct][tg >> 3][at]) = w;
-                if constexpr (LO) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = wl[i][c];
-                    *reinterpret_cast<half4 *>(&B.W[1][ct][tg >> 3][at]) = w;
-                }
+                for (int l = 0; l < NK; ++l) *reinterpret_cast<half4 *>(&sh.W[l][ct][tg >> 3][at]) = w[u][l][c];
             }
         }
-#pragma unroll
-        for (int i = 0; i < kTP / 256; ++i) B.TP[tid + 256 * i] = tp[i];
-        if (tid < kMeta) reinterpret_cast<uint4 *>(&B.m)[tid] = meta;
+        pieces(tid, [&](u32x4 &x, int i) { sh.tp[i] = x; });
     }
 };
 
-__device__ inline half8 frag(const _Float16 *p) { return *reinterpret_cast<const half8 *>(p); }
+// Places in LDS whose constant offsets go into the reading instructions.  They are
+// formed anew where they are used: the compiler would otherwise keep the sums of place
+// and offset, dozens of registers, over the whole loop.
+typedef __attribute__((address_space(3))) const _Float16 *lds_half;
+typedef __attribute__((address_space(3))) const float *lds_float;
+
+__device__ inline lds_half half_at(const void *p, int at) {
+    lds_half q = (lds_half)p + at;
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline lds_float float_at(const void *p, int at) {
+    lds_float q = (lds_float)p + at;
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline half8 frag(lds_half p) { return *(__attribute__((address_space(3))) const half8 *)p; }
 
 // Two result tiles (rows 16 m.. and 16 m + 16..) times s as a right operand.
 __device__ inline void right(const floatx4 &x, const floatx4 &y, float s, half8 &hi, half8 &lo) {
@@ -233,230 +267,235 @@ __device__ inline float column_max(const floatx4 (&x)[n]) {
     return max_groups(m);
 }
 
-__device__ inline floatx4 row_factors(const float *p) {
-    const float4 x = *reinterpret_cast<const float4 *>(p);
-    return floatx4{x.x, x.y, x.z, x.w};
+__device__ inline floatx4 row_factors(lds_float p) {
+    return *(__attribute__((address_space(3))) const floatx4 *)p;
+}
+// Of the factors at `member` of ChunkMeta, those of row tile rt.
+constexpr int factors(size_t member, int rt) { return (int)(member / sizeof(float)) + 16 * rt; }
+
+// A lower triangular left operand (fragments at t, lo parts kTri further) times
+// a column block; `undo` takes the block's scale away.  FULL: with the lo parts.
+template <bool FULL>
+__device__ inline void lower(lds_half t, const floatx4 (&X)[4], floatx4 (&Y)[4], float &undo) {
+    const float s = scale_to(column_max(X), 13, undo);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        __builtin_amdgcn_sched_barrier(0);
+        half8 hi, lo, th[4];
+        right(X[2 * ks], X[2 * ks + 1], s, hi, lo);
+#pragma unroll
+        for (int rt = 2 * ks; rt < 4; ++rt) th[rt] = frag(t + tri(rt, ks) * kFrag);
+#pragma unroll
+        for (int rt = 2 * ks; rt < 4; ++rt) Y[rt] = mfma16(th[rt], hi, Y[rt]);
+        if constexpr (FULL) {
+#pragma unroll
+            for (int rt = 2 * ks; rt < 4; ++rt) Y[rt] = mfma16(th[rt], lo, Y[rt]);
+#pragma unroll
+            for (int rt = 2 * ks; rt < 4; ++rt) th[rt] = frag(t + (kTri + tri(rt, ks)) * kFrag);
+#pragma unroll
+            for (int rt = 2 * ks; rt < 4; ++rt) Y[rt] = mfma16(th[rt], hi, Y[rt]);
+        }
+    }
 }
 
-template <int DK, int DV, int NT, bool KEYVEC, bool BF16>
-__global__ void __launch_bounds__(512) k_chunk_fwd(const ChunkArgs A) {
-    constexpr bool LO = KEYVEC || !BF16;
-    typedef FwdShared<DK, LO> Shared;
-    constexpr int KS = Shared::KS, CT = Shared::CT, NBUF = Shared::NBUF;
+template <int DK, int DV, int NW, bool KEYVEC, bool BF16>
+__global__ void __launch_bounds__((64 * NW + Producer<DK, KEYVEC, BF16>::PT)) k_chunk_fwd(const ChunkArgs A) {
+    typedef FwdShared<DK, KEYVEC, BF16> Shared;
+    typedef typename Raw4<BF16>::type raw;
+    constexpr int KS = Shared::KS, CT = Shared::CT, NK = Shared::NK, NQ = Shared::NQ;
     __shared__ Shared sh;
     const int H = A.s.H, h = blockIdx.y, b = blockIdx.z;
     int t0, t1;
     seq_range(A.s, b, t0, t1);
     const int nc = (t1 - t0 + kC - 1) / kC;
-    const ChunkPrep *entry = A.prep + (size_t)(t0 / kC + b) * H + h;
 
-    if (threadIdx.x >= 256) {
-        const int tid = threadIdx.x - 256;
+    if (threadIdx.x >= 64 * NW) {
+        if (nc == 0) return;
+        const size_t entry = (size_t)(t0 / kC + b) * H + h;
+        const int tid = threadIdx.x - 64 * NW;
         Producer<DK, KEYVEC, BF16> p;
         auto load = [&](int c) {
-            if (c < nc) p.load(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry + (size_t)c * H, tid);
+            p.load(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry + (size_t)c * H, tid);
         };
         load(0);
-        if constexpr (NBUF == 2) {
-            if (nc) p.write(sh, 0, tid);
-            load(1);
-            for (int c = 0; c < nc; ++c) {
-                __syncthreads();
-                if (c + 1 < nc) p.write(sh, (c + 1) & 1, tid);
-                load(c + 2);
-            }
-        } else {
-            if (nc) p.groups(sh, tid);
-            for (int c = 0; c < nc; ++c) {
-                __syncthreads();
-                p.write(sh, 0, tid);
-                __syncthreads();
-                load(c + 1);
-                if (c + 1 < nc) p.groups(sh, tid);
-            }
+        p.load_tp(A.prep + entry, tid);
+        p.write_kq(sh, 0, tid);
+        if (nc > 1) load(1);
+        for (int c = 0; c < nc; ++c) {
+            lds_barrier();               // K and Q of c stand; T, P, K^T of c - 1 are done with
+            p.write_tpw(sh, tid);
+            if (c + 1 < nc) p.load_tp(A.prep + entry + (size_t)(c + 1) * H, tid);
+            lds_barrier();               // T, P, K^T of c stand; K and Q of c are done with
+            if (c + 1 < nc) p.write_kq(sh, (c + 1) & 1, tid);
+            if (c + 2 < nc) load(c + 2);
         }
         return;
     }
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.x * 4 + wave) * 16 * NT + c16;  // of the first tile
-    floatx4 S[NT][CT];
-    const size_t state0 = ((size_t)b * H + h) * DK * DV;
+    const int col0 = (blockIdx.x * NW + wave) * 16;
+    floatx4 S[CT];
+    const size_t state0 = ((size_t)b * H + h) * DK * DV + col0;
+    uint32_t at0 = 4 * g * DV + c16;     // of the lane's first value in the state
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[nt][ct][r] =
-                    A.initial ? A.initial[state0 + (size_t)(16 * ct + 4 * g + r) * DV + col + 16 * nt] : 0.f;
+        for (int r = 0; r < 4; ++r) S[ct][r] = A.initial ? (A.initial + state0 + (16 * ct + r) * DV)[at0] : 0.f;
+    asm volatile("" : "+v"(at0));        // (what is formed from it for the last states is formed there)
 
-    float v[NT][16];
+    // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
+    const int row0 = 4 * g + (c16 & 3);
+    const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
+    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
+    raw v[4];                            // of the next chunk; past the last token its row again
     auto load_v = [&](int c) {
+        const raw *base = static_cast<const raw *>(A.s.v) + (size_t)(t0 + c * kC) * row_step + col4;
+        const int n = t1 - t0 - c * kC;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int t = t0 + c * kC + 16 * (i >> 2) + 4 * g + (i & 3);
-                v[nt][i] = 0.f;
-                if (t < t1) {
-                    const size_t at = ((size_t)t * H + h) * DV + col + 16 * nt;
-                    if constexpr (BF16)
-                        v[nt][i] = __uint_as_float((uint32_t)static_cast<const uint16_t *>(A.s.v)[at] << 16);
-                    else v[nt][i] = static_cast<const float *>(A.s.v)[at];
-                }
-            }
+        for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + row0, n - 1) * row_step];
     };
     if (nc) load_v(0);
 
     for (int c = 0; c < nc; ++c) {
-        __syncthreads();
-        if constexpr (NBUF == 1) __syncthreads();
-        const auto &B = sh.buf[NBUF == 2 ? c & 1 : 0];
-        const _Float16 *tp = reinterpret_cast<const _Float16 *>(B.TP);
-        floatx4 R[NT][4], O[NT][4];
-        float inv[NT];
+        lds_barrier();
+        const lds_float m = float_at(&sh.m[c & 1], 4 * g);
+        floatx4 R[4], O[4];
+        float undo;
         {
-            float s[NT];
+            const float s = scale_to(column_max(S), 13, undo);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt] = scale_to(column_max(S[nt]), 13, inv[nt]);
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt) R[nt][rt] = O[nt][rt] = floatx4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int rt = 0; rt < 4; ++rt) R[rt] = O[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                half8 hi[NT], lo[NT];
+                half8 hi, lo;
+                right(S[2 * ks], S[2 * ks + 1], s, hi, lo);
+                const lds_half kq = half_at(&sh.K, place_k(c16, g, ks));
+                half8 f[4];
+                // (an operand's four fragments at a time: more of them in flight spill)
+                auto rows = [&](int from, floatx4 (&Y)[4], bool both) {
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) right(S[nt][2 * ks], S[nt][2 * ks + 1], s[nt], hi[nt], lo[nt]);
-                const int at = place_k(c16, g, ks);
+                    for (int rt = 0; rt < 4; ++rt) f[rt] = frag(kq + (from + rt * KS + ks) * kFrag);
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    const half8 kh = frag(&B.K[0][rt][ks][at]), qh = frag(&B.Q[0][rt][ks][at]);
+                    for (int rt = 0; rt < 4; ++rt) Y[rt] = mfma16(f[rt], hi, Y[rt]);
+                    if (both) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        R[nt][rt] = mfma16(kh, hi[nt], R[nt][rt]);
-                        O[nt][rt] = mfma16(qh, hi[nt], O[nt][rt]);
-                        R[nt][rt] = mfma16(kh, lo[nt], R[nt][rt]);
-                        O[nt][rt] = mfma16(qh, lo[nt], O[nt][rt]);
+                        for (int rt = 0; rt < 4; ++rt) Y[rt] = mfma16(f[rt], lo, Y[rt]);
                     }
-                    if constexpr (LO) {
-                        const half8 kl = frag(&B.K[1][rt][ks][at]), ql = frag(&B.Q[1][rt][ks][at]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            R[nt][rt] = mfma16(kl, hi[nt], R[nt][rt]);
-                            O[nt][rt] = mfma16(ql, hi[nt], O[nt][rt]);
-                        }
-                    }
-                }
+                };
+                rows(0, R, true);
+                rows(4 * KS * NK, O, NQ == 2);
+                if constexpr (NK == 2) rows(4 * KS, R, false);
+                if constexpr (NQ == 2) rows(4 * KS * (NK + 1), O, false);
             }
         }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const floatx4 rk = row_factors(&B.m.rk[16 * rt + 4 * g]), rq = row_factors(&B.m.rq[16 * rt + 4 * g]);
+            __builtin_amdgcn_sched_barrier(0);
+            const floatx4 rk = row_factors(m + factors(offsetof(ChunkMeta, rk), rt)),
+                          rq = row_factors(m + factors(offsetof(ChunkMeta, rq), rt));
+            float x[4];
+            widen(v[rt], x);
+            quad_transpose(x);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    // (one factor after the other: their product may underflow where the value does not)
-                    R[nt][rt][r] = __builtin_fmaf(-(R[nt][rt][r] * rk[r]), inv[nt], v[nt][4 * rt + r]);
-                    O[nt][rt][r] = (O[nt][rt][r] * rq[r]) * inv[nt];
-                }
+            for (int r = 0; r < 4; ++r) {
+                // (one factor after the other: their product may underflow where the value does not)
+                R[rt][r] = __builtin_fmaf(-(R[rt][r] * rk[r]), undo, x[r]);
+                O[rt][r] = (O[rt][r] * rq[r]) * undo;
+            }
         }
         if (c + 1 < nc) load_v(c + 1);
-        // a lower triangular left operand (T at 0, P at 1) times a column block
-        auto lower = [&](int which, const floatx4 (&X)[4], floatx4 (&Y)[4], float &undo) {
-            const float s = scale_to(column_max(X), 13, undo);
-            const _Float16 *t = tp + which * 2 * kTri * kFrag + lane * 8;
+        lds_barrier();
+        floatx4 u[4], y[4];
+        const lds_half t = half_at(&sh.tp, lane * 8);
+        lower<true>(t, R, u, undo);
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int rt = 0; rt < 4; ++rt) {
+            const floatx4 f = row_factors(m + factors(offsetof(ChunkMeta, rt), rt));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[rt][r] = (u[rt][r] * f[r]) * undo;
+        }
+        lower<NQ == 2>(t + 2 * kTri * kFrag, u, y, undo);
+        raw *out = static_cast<raw *>(A.o) + (size_t)(t0 + c * kC) * row_step + col4;
+        const int n = t1 - t0 - c * kC;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            __builtin_amdgcn_sched_barrier(0);
+            const floatx4 f = row_factors(m + factors(offsetof(ChunkMeta, rp), rt)),
+                          w = row_factors(m + factors(offsetof(ChunkMeta, rw), rt));
+            float x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = __builtin_fmaf(y[rt][r] * f[r], undo, O[rt][r]);
+                u[rt][r] *= w[r];
+            }
+            quad_transpose(x);
+            raw z;
+            narrow(x, z);
+            if (16 * rt + row0 < n) out[(uint32_t)(16 * rt + row0) * row_step] = z;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const float s = scale_to(column_max(u), 13, undo);
+        half8 hi[2], lo[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) right(u[2 * ks], u[2 * ks + 1], s, hi[ks], lo[ks]);
+        lds_half wb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wb[i] = half_at(&sh.W, place_w(c16, g, i));
+#pragma unroll
+        for (int c0 = 0; c0 < CT; c0 += 4) {
+            __builtin_amdgcn_sched_barrier(0);
+            floatx4 z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                half8 hi, lo;
-                right(X[2 * ks], X[2 * ks + 1], s, hi, lo);
+                half8 wf[4];
 #pragma unroll
-                for (int rt = 2 * ks; rt < 4; ++rt) {
-                    const half8 th = frag(t + tri(rt, ks) * kFrag), tl = frag(t + (kTri + tri(rt, ks)) * kFrag);
-                    Y[rt] = mfma16(th, hi, Y[rt]);
-                    Y[rt] = mfma16(th, lo, Y[rt]);
-                    Y[rt] = mfma16(tl, hi, Y[rt]);
+                for (int i = 0; i < 4; ++i) wf[i] = frag(wb[i] + ((c0 + i) * 2 + ks) * kFrag);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = mfma16(wf[i], hi[ks], z[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = mfma16(wf[i], lo[ks], z[i]);
+                if constexpr (NK == 2) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        z[i] = mfma16(frag(wb[i] + ((CT + c0 + i) * 2 + ks) * kFrag), hi[ks], z[i]);
                 }
             }
-        };
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            floatx4 u[4], y[4];
-            float undo;
-            lower(0, R[nt], u, undo);
+            for (int i = 0; i < 4; ++i) {
+                const floatx4 d = row_factors(m + factors(offsetof(ChunkMeta, dec), c0 + i));
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const floatx4 f = row_factors(&B.m.rt[16 * rt + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) u[rt][r] = (u[rt][r] * f[r]) * undo;
-            }
-            lower(1, u, y, undo);
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const floatx4 f = row_factors(&B.m.rp[16 * rt + 4 * g]);
-                const floatx4 w = row_factors(&B.m.rw[16 * rt + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float o = __builtin_fmaf(y[rt][r] * f[r], undo, O[nt][rt][r]);
-                    const int t = t0 + c * kC + 16 * rt + 4 * g + r;
-                    if (t < t1) {
-                        const size_t at = ((size_t)t * H + h) * DV + col + 16 * nt;
-                        if constexpr (BF16) static_cast<__bf16 *>(A.o)[at] = (__bf16)o;
-                        else static_cast<float *>(A.o)[at] = o;
-                    }
-                    u[rt][r] *= w[r];
-                }
-            }
-            const float s = scale_to(column_max(u), 13, undo);
-            half8 hi[2], lo[2];
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) right(u[2 * ks], u[2 * ks + 1], s, hi[ks], lo[ks]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                floatx4 z = {0.f, 0.f, 0.f, 0.f};
-                const int at = place_w(c16, g, ct);
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const half8 wh = frag(&B.W[0][ct][ks][at]);
-                    z = mfma16(wh, hi[ks], z);
-                    z = mfma16(wh, lo[ks], z);
-                    if constexpr (LO) z = mfma16(frag(&B.W[1][ct][ks][at]), hi[ks], z);
-                }
-                const floatx4 d = row_factors(&B.m.dec[16 * ct + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[nt][ct][r] = __builtin_fmaf(z[r], undo, S[nt][ct][r] * d[r]);
+                for (int r = 0; r < 4; ++r) S[c0 + i][r] = __builtin_fmaf(z[i][r], undo, S[c0 + i][r] * d[r]);
             }
         }
     }
     if (!A.last) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                A.last[state0 + (size_t)(16 * ct + 4 * g + r) * DV + col + 16 * nt] = S[nt][ct][r];
+        for (int r = 0; r < 4; ++r) (A.last + state0 + (16 * ct + r) * DV)[at0] = S[ct][r];
 }
 
-template <int DK, int DV, int NT>
+template <int DK, int DV, int NW>
 void go(const ChunkArgs &a, bool keyvec, bool bf16, hipStream_t s) {
-    const dim3 grid(DV / (64 * NT), (unsigned)a.s.H, (unsigned)a.s.B);
-    if (keyvec && bf16) k_chunk_fwd<DK, DV, NT, true, true><<<grid, 512, 0, s>>>(a);
-    else if (keyvec) k_chunk_fwd<DK, DV, NT, true, false><<<grid, 512, 0, s>>>(a);
-    else if (bf16) k_chunk_fwd<DK, DV, NT, false, true><<<grid, 512, 0, s>>>(a);
-    else k_chunk_fwd<DK, DV, NT, false, false><<<grid, 512, 0, s>>>(a);
+    const dim3 grid(DV / (16 * NW), (unsigned)a.s.H, (unsigned)a.s.B);
+    constexpr int lo = 64 * NW + Producer<DK, true, true>::PT, plain = 64 * NW + Producer<DK, false, true>::PT;
+    if (keyvec && bf16) k_chunk_fwd<DK, DV, NW, true, true><<<grid, lo, 0, s>>>(a);
+    else if (keyvec) k_chunk_fwd<DK, DV, NW, true, false><<<grid, lo, 0, s>>>(a);
+    else if (bf16) k_chunk_fwd<DK, DV, NW, false, true><<<grid, plain, 0, s>>>(a);
+    else k_chunk_fwd<DK, DV, NW, false, false><<<grid, lo, 0, s>>>(a);
 }
 
 template <int DK>
 void go_dv(const ChunkArgs &a, int dv, bool keyvec, bool bf16, hipStream_t s) {
     const bool few = (int64_t)a.s.B * a.s.H < 256;  // fewer pairs than compute units
-    if (dv == 64) go<DK, 64, 1>(a, keyvec, bf16, s);
-    else if (few) go<DK, 128, 1>(a, keyvec, bf16, s);
-    else go<DK, 128, 2>(a, keyvec, bf16, s);
+    if (dv == 64) go<DK, 64, 4>(a, keyvec, bf16, s);
+    else if (few) go<DK, 128, 4>(a, keyvec, bf16, s);
+    else go<DK, 128, 8>(a, keyvec, bf16, s);
 }
 
 }  // namespace

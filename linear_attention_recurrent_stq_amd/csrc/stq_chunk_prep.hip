@@ -32,20 +32,19 @@ struct PrepShared {
 };
 
 // Row scales of K and Q: thread (row, quarter) looks at a quarter of the row.
+// Rows past the last token take its scales: the pass of the state reads its row there.
 template <int DK, bool BF16>
 __device__ inline void row_scales(const SeqArgs &s, int h, int first, int n, ChunkMeta &m, PrepShared &sh) {
     constexpr int W = DK / 4;
     const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
-    float mk = 0.f, mq = 0.f;
-    if (row < n) {
-        const size_t at = ((size_t)(first + row) * s.H + h) * DK + part * W;
-        float x[W];
-        load_row<BF16>(s.k, at, x);
+    float mk = 0.f, mq = 0.f, x[W], y[W];
+    const size_t at = ((size_t)(first + min(row, n - 1)) * s.H + h) * DK + part * W;
+    load_row<BF16>(s.k, at, x);
+    load_row<BF16>(s.q, at, y);
 #pragma unroll
-        for (int i = 0; i < W; ++i) mk = fmaxf(mk, fabsf(x[i]));
-        load_row<BF16>(s.q, at, x);
-#pragma unroll
-        for (int i = 0; i < W; ++i) mq = fmaxf(mq, fabsf(x[i]));
+    for (int i = 0; i < W; ++i) {
+        mk = fmaxf(mk, fabsf(x[i]));
+        mq = fmaxf(mq, fabsf(y[i]));
     }
     mk = fmaxf(mk, __shfl_xor(mk, 1));
     mk = fmaxf(mk, __shfl_xor(mk, 2));
@@ -303,6 +302,24 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
         out.m.rk[tid] = sh.ik[tid];
         out.m.rq[tid] = sh.iq[tid];
         out.m.rw[tid] = sh.ik[tid];
+    }
+    {  // gate products before and after each four tokens
+        ChunkGates &o = A.gates[(size_t)blockIdx.x * s.H + h];
+        const int c = tid % DK;
+        float run = 1.f;
+        if (tid < DK) {
+#pragma unroll 16
+            for (int i = 0; i < kC; ++i) {
+                if (i % 4 == 0) o.pre[i / 4][c] = run;
+                run *= Ga[i][c];
+            }
+        } else if (tid < 2 * DK) {
+#pragma unroll 16
+            for (int i = kC - 1; i >= 0; --i) {
+                if (i % 4 == 3) o.suf[i / 4][c] = run;
+                run *= Ga[i][c];
+            }
+        }
     }
     // splits at 16 and 48: rows of blocks 0 and 2 carry the product up to the
     // block's end, rows of blocks 1 and 3 the product from the block's start

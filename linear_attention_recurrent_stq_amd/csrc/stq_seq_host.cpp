@@ -124,7 +124,9 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
     if (stq_status s = check_sizes(rule, B, N)) return s;
     if (!bytes) return fail(STQ_ERR_INVALID, "bytes is NULL");
     if (backward) return fail(STQ_ERR_UNSUPPORTED, "no backward pass");
-    *bytes = sizeof(stq::ChunkPrep) * (size_t)stq::chunk_slots(N, B) * rule->H;
+    size_t each = sizeof(stq::ChunkPrep);
+    if (rule->gate == STQ_GATE_KEYVEC) each += sizeof(stq::ChunkGates);
+    *bytes = each * (size_t)stq::chunk_slots(N, B) * rule->H;
     return STQ_OK;
 }
 
@@ -150,6 +152,7 @@ stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const i
     a.o = d_o;
     a.prep = static_cast<stq::ChunkPrep *>(d_workspace);
     a.slots = stq::chunk_slots(N, B);
+    a.gates = reinterpret_cast<stq::ChunkGates *>(a.prep + (size_t)a.slots * rule->H);
     const bool keyvec = rule->gate == STQ_GATE_KEYVEC, bf16 = rule->io_dtype == STQ_BF16;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (N > 0)
