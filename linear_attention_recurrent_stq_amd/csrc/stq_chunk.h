@@ -75,16 +75,25 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
+// A wave's number in its workgroup, in a scalar register: branches on it are the whole
+// wave's (matrix instructions write their results whatever lanes are on).
+__device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // The chunk of slot x: its sequence, first token and number of tokens; 0 tokens
-// where the slot holds none.
+// where the slot holds none.  Called by whole waves: the sequence is searched for 64
+// candidates at a time.
 __device__ inline int chunk_of_slot(const SeqArgs &s, int x, int &b, int &first) {
-    int lo = 0, hi = s.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (min(max(s.cu[mid], 0), s.N) / kC + mid <= x) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = s.B;
+    while (n > 1) {
+        const int step = (n + 63) >> 6, at = lane * step;
+        bool ok = false;
+        if (at < n) ok = min(max(s.cu[lo + at], 0), s.N) / kC + lo + at <= x;
+        const int i = max(__popcll(__ballot(ok)), 1) - 1;  // the last candidate at or before x
+        lo += i * step;
+        n = min(step, n - i * step);
     }
-    b = lo;
+    b = __builtin_amdgcn_readfirstlane(lo);
     int t0, t1;
     seq_range(s, b, t0, t1);
     const int c = x - (t0 / kC + b);
@@ -120,6 +129,14 @@ __device__ inline float max_groups(float x) {
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+
+// The value of another lane of the row of 16 (`old` where there is none).
+template <int ctrl>
+__device__ inline float dpp(float x, float old = 0.f) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), ctrl, 0xf, 0xf, false));
+}
+constexpr int kShl = 0x100, kShr = 0x110, kRor = 0x120, kBcast = 0x150;  // lane i + n, i - n, i - n mod 16, n
+constexpr int quad(int a, int b, int c, int d) { return a | b << 2 | c << 4 | d << 6; }
 
 // x[j] of lane i of a quad becomes x[i] of lane j.
 template <int ctrl>

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__((64 * NW + Producer<DK, KEYVEC, BF16>::PT)) k_
         return;
     }
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
     const int col0 = (blockIdx.x * NW + wave) * 16;
     floatx4 S[CT];
     const size_t state0 = ((size_t)b * H + h) * DK * DV + col0;

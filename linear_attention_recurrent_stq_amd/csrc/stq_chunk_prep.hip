@@ -1,111 +1,160 @@
 // What the chunks of a batch need before the state passes through them:
 // T and P (stq_chunk.h) and the factors of every token.  One workgroup of four
-// waves per (chunk, head); all chunks at once.
+// waves per (chunk, head), all chunks at once; wave w holds rows 16 w .. 16 w + 15 as
+// matrix operands, lane (r, g) the row r's channels 32 s + 8 g .. + 7.
 //
-// Scalar gates: A and P are K K^T and Q K^T times D_ij = prod_{j<s<=i} a_s.  The
-// products of bf16 rows run on bf16 matrix instructions (exact products, fp32
-// sums), fp32 rows on fp32 ones.  D is formed by running products down its
-// columns, 16 rows at a time by 256 threads.
+// A and P are lower triangular, in 16x16 blocks (I, J).  With pre_i the product of
+// the gates from its block's start to i, suf_j of those after j in its block, and
+// mid the product of the blocks between, a block off the diagonal has the decay
+// pre_i mid suf_j: products of gates only, at most 1.
 //
-// Key-vector gates: the decay sits inside the sum over channels.  It is split at
-// a token between i and j: at 32 for the lower left quarter, at 16 and 48 for
-// the blocks next to the diagonal ones, so that both factors, prod from the
-// split to i and prod from j to the split, are products of gates (at most 1)
-// and the block is one matrix product (fp32 matrix instructions).  The four
-// 16x16 blocks on the diagonal have no such split: a lane holds k_j for 32
-// channels, multiplies a_i in for each next i and forms the dot products with k_i
-// and q_i; they are vector code.
+// Scalar gates: A and P are K K^T and Q K^T times the decay; bf16 rows multiply
+// exactly on bf16 matrix instructions, fp32 rows on fp32 ones.  Inside a diagonal block
+// the decay is a running product down each column.
+//
+// Key-vector gates: the decay sits inside the sum over channels, so the rows are
+// multiplied by it first, (q, k) pre (mid) against k suf.  A diagonal block is cut the
+// same way, at 8 and at 4 (X of the later half's rows and, in the rows that it
+// leaves free, Q's: one product a cut), down to 4x4 blocks, which are vector code:
+// the three earlier rows of a quad of lanes are read across lanes.  Products of gates
+// within 2, 4, 8 and 16 rows come from one scan across the lanes of a row of 16.  These
+// operands are scaled fp16 pairs.
 //
 // T: the 16x16 diagonal blocks of I + diag(beta) A are inverted by forward
 // substitution, a wave each; a wave then builds one block column of the inverse,
 // T_IJ = -X_I sum_m M_Im T_mJ, with fp32 matrix instructions.  A result tile is a
 // right operand in the registers it is in, so the chain needs no exchange.
+//
+// Rows past a chunk's last token repeat it, with beta 0 and gate 1: their rows and
+// columns of T are 0, and their outputs are not stored.
 #include "stq_chunk.h"
 
 namespace stq {
 namespace {
 
-constexpr int LD = kC + 4;  // row stride of 64x64 matrices in LDS
+constexpr int LD = kC + 4;  // row stride of M in LDS
 
-struct PrepShared {
-    float be[kC], ik[kC], iq[kC];    // beta; inverse scales of K and Q rows
+// A choice whose both values are formed by every lane: a value read across lanes
+// inside a branch would find the other lanes switched off.
+__device__ inline float pick(bool c, float x, float y) { return c ? x : y; }
+
+// max over the lanes of a row of 16
+__device__ inline float max_row(float x) {
+    x = fmaxf(x, dpp<kRor + 8>(x));
+    x = fmaxf(x, dpp<kRor + 4>(x));
+    x = fmaxf(x, dpp<kRor + 2>(x));
+    return fmaxf(x, dpp<kRor + 1>(x));
+}
+__device__ inline float sum_groups(float x) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline floatx4 four(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
+
+// Eight consecutive channels as they are in memory.
+template <bool BF16> struct Row8;
+template <> struct Row8<true> {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 w;
+    __device__ void load(const void *p, size_t at) {
+        w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + at);
+    }
+    __device__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+};
+template <> struct Row8<false> {
+    floatx4 x, y;
+    __device__ void load(const void *p, size_t at) {
+        x = four(static_cast<const float *>(p) + at);
+        y = four(static_cast<const float *>(p) + at + 4);
+    }
+    __device__ float get(int i) const { return i < 4 ? x[i] : y[i - 4]; }
 };
 
-// Row scales of K and Q: thread (row, quarter) looks at a quarter of the row.
-// Rows past the last token take its scales: the pass of the state reads its row there.
 template <int DK, bool BF16>
-__device__ inline void row_scales(const SeqArgs &s, int h, int first, int n, ChunkMeta &m, PrepShared &sh) {
-    constexpr int W = DK / 4;
-    const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
-    float mk = 0.f, mq = 0.f, x[W], y[W];
-    const size_t at = ((size_t)(first + min(row, n - 1)) * s.H + h) * DK + part * W;
-    load_row<BF16>(s.k, at, x);
-    load_row<BF16>(s.q, at, y);
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        mk = fmaxf(mk, fabsf(x[i]));
-        mq = fmaxf(mq, fabsf(y[i]));
-    }
-    mk = fmaxf(mk, __shfl_xor(mk, 1));
-    mk = fmaxf(mk, __shfl_xor(mk, 2));
-    mq = fmaxf(mq, __shfl_xor(mq, 1));
-    mq = fmaxf(mq, __shfl_xor(mq, 2));
-    if (part == 0) {
-        float ik, iq;
-        m.sk[row] = scale_to(mk, 10, ik);
-        m.sq[row] = scale_to(mq, 10, iq);
-        sh.ik[row] = ik;
-        sh.iq[row] = iq;
-        sh.be[row] = row < n ? s.beta[(size_t)(first + row) * s.H + h] : 0.f;
-    }
-}
+struct Rows {
+    Row8<BF16> k[DK / 32], q[DK / 32];
+    size_t at;                       // of the lane's first channel
+    float sk, ik, sq, iq;            // scales of the row and what undoes them
 
-// A row of a 64x64 LDS matrix, thread (row, 16 columns), as scaled fp16 pairs
-// in fragment order.
-__device__ inline void store_tri(const float (*X)[LD], uint16_t (&to)[2][kTri][kFrag], float *undo) {
-    const int i = threadIdx.x >> 2, qq = threadIdx.x & 3, rt = i >> 4;
-    const int ks = qq >> 1;
-    const bool kept = ks <= rt / 2;  // what lies further right is 0 and has no fragment
-    float x[16], m = 0.f;
+    __device__ void load(const SeqArgs &s, int h, int first, int n) {
+        const int lane = threadIdx.x & 63, row = 16 * wave_index() + (lane & 15);
+        at = ((size_t)(first + min(row, n - 1)) * s.H + h) * DK + 8 * (lane >> 4);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        x[c] = kept ? X[i][16 * qq + c] : 0.f;
-        m = fmaxf(m, fabsf(x[c]));
-    }
-    m = fmaxf(m, __shfl_xor(m, 1));
-    m = fmaxf(m, __shfl_xor(m, 2));
-    float inv;
-    const float s = scale_to(m, 10, inv);
-    if (qq == 0) undo[i] = inv;
-    if (!kept) return;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        half4 hi, lo;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            _Float16 a, b;
-            split(x[4 * g + e], s, a, b);
-            hi[e] = a;
-            lo[e] = b;
+        for (int i = 0; i < DK / 32; ++i) {
+            k[i].load(s.k, at + 32 * i);
+            q[i].load(s.q, at + 32 * i);
         }
-        const int at = ((i & 15) + 16 * g) * 8 + (qq & 1) * 4;
-        *reinterpret_cast<half4 *>(&to[0][tri(rt, ks)][at]) = hi;
-        *reinterpret_cast<half4 *>(&to[1][tri(rt, ks)][at]) = lo;
     }
+    __device__ void scales() {
+        float mk = 0.f, mq = 0.f;
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                mk = fmaxf(mk, fabsf(k[i].get(e)));
+                mq = fmaxf(mq, fabsf(q[i].get(e)));
+            }
+        sk = scale_to(max_groups(mk), 10, ik);
+        sq = scale_to(max_groups(mq), 10, iq);
+    }
+};
+
+// A 16x16 result tile times its rows' scales s, as fp16 pairs in fragment order;
+// tile (I, J) of a lower triangular matrix.
+__device__ inline void store_tile(floatx4 x, floatx4 s, int I, int J, uint16_t (&to)[2][kTri][kFrag]) {
+    const int c16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    float y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[r] = x[r] * s[r];
+    quad_transpose(y);
+    half4 hi, lo;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        hi[r] = (_Float16)y[r];
+        lo[r] = (_Float16)(y[r] - (float)hi[r]);
+    }
+    const int f = I < 2 ? I : 2 + 2 * (I - 2) + (J >> 1);
+    const int at = (4 * g + (c16 & 3) + 16 * (c16 >> 2)) * 8 + (J & 1) * 4;
+    *reinterpret_cast<half4 *>(&to[0][f][at]) = hi;
+    *reinterpret_cast<half4 *>(&to[1][f][at]) = lo;
 }
 
-// From M = diag(beta) A (strictly lower; what lies above the diagonal is not
-// read) and P in LDS to what the entry holds.  T is written over `Tx`.
-__device__ inline void finish(const float (*M)[LD], const float (*Px)[LD], float (*Tx)[LD], float (*X)[20],
-                              const float *be, ChunkPrep &out) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
+// Row w of P's blocks.
+__device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
+    const int lane = threadIdx.x & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
+    floatx4 s, inv;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float m = 0.f, x;
+#pragma unroll
+        for (int J = 0; J < 4; ++J) m = fmaxf(m, J <= w ? fabsf(p[J][r]) : 0.f);
+        s[r] = scale_to(max_row(m), 10, x);
+        inv[r] = x;
+    }
+#pragma unroll
+    for (int J = 0; J < 4; ++J)
+        if (J <= (w | 1)) store_tile(J <= w ? p[J] : floatx4{0.f, 0.f, 0.f, 0.f}, s, w, J, out.P);
+    if (c16 == 0) *reinterpret_cast<floatx4 *>(&out.m.rp[16 * w + 4 * g]) = inv;
+}
+
+// From M = diag(beta) A in LDS (strictly lower; what lies above the diagonal is
+// not read) to T.
+__device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)[kC], const float *be, ChunkPrep &out) {
+    const int lane = threadIdx.x & 63, wave = wave_index(), j = lane & 15, g = lane >> 4;
     // inverse of the diagonal block `wave`, column j
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         float s = i == j ? 1.f : 0.f;
 #pragma unroll
-        for (int m = 0; m < i; ++m) s = __builtin_fmaf(-M[16 * wave + i][16 * wave + m], x[m], s);
+        for (int m = 0; m < i; m += 4) {
+            const floatx4 f = four(&M[16 * wave + i][16 * wave + m]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e < i) s = __builtin_fmaf(-f[e], x[m + e], s);
+        }
         x[i] = s;
     }
     if (g == 0) {
@@ -126,311 +175,352 @@ __device__ inline void finish(const float (*M)[LD], const float (*Px)[LD], float
 #pragma unroll
             for (int m = 0; m < I; ++m) {
                 if (m < wave) continue;
-                const float4 a = *reinterpret_cast<const float4 *>(&M[16 * I + j][16 * m + 4 * g]);
-                y = mfma_f32(a.x, t[m][0], y);
-                y = mfma_f32(a.y, t[m][1], y);
-                y = mfma_f32(a.z, t[m][2], y);
-                y = mfma_f32(a.w, t[m][3], y);
+                const floatx4 a = four(&M[16 * I + j][16 * m + 4 * g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y = mfma_f32(a[e], t[m][e], y);
             }
-            const float4 a = *reinterpret_cast<const float4 *>(&X[16 * I + j][4 * g]);
-            z = mfma_f32(-a.x, y[0], z);
-            z = mfma_f32(-a.y, y[1], z);
-            z = mfma_f32(-a.z, y[2], z);
-            z = mfma_f32(-a.w, y[3], z);
+            const floatx4 a = four(&X[16 * I + j][4 * g]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z = mfma_f32(-a[e], y[e], z);
             t[I] = z;
         }
     }
     const float b = be[16 * wave + j];
 #pragma unroll
-    for (int I = 0; I < 4; ++I)
+    for (int I = 0; I < 4; ++I) {
+        floatx4 m;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) Tx[16 * I + 4 * g + r][16 * wave + j] = t[I][r] * b;
+        for (int r = 0; r < 4; ++r) {
+            t[I][r] *= b;
+            m[r] = max_row(fabsf(t[I][r]));
+        }
+        if (j == 0) *reinterpret_cast<floatx4 *>(&tm[wave][16 * I + 4 * g]) = m;
+    }
     __syncthreads();
-    store_tri(Tx, out.T, out.m.rt);
-    store_tri(Px, out.P, out.m.rp);
-}
-
-// Eight channels of row `row` for a matrix instruction; 0 past the last token.
-template <int DK>
-__device__ inline bf16x8 frag_bf16(const void *p, const SeqArgs &s, int h, int first, int n, int row, int c) {
-    union { uint4 w; bf16x8 v; } x;
-    x.w = make_uint4(0, 0, 0, 0);
-    if (row < n)
-        x.w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) +
-                                               ((size_t)(first + row) * s.H + h) * DK + c);
-    return x.v;
-}
-template <int DK>
-__device__ inline float4 frag_f32(const void *p, const SeqArgs &s, int h, int first, int n, int row, int c) {
-    if (row >= n) return make_float4(0.f, 0.f, 0.f, 0.f);
-    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) +
-                                             ((size_t)(first + row) * s.H + h) * DK + c);
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+        if ((I | 1) < wave) continue;
+        floatx4 m = four(&tm[0][16 * I + 4 * g]), s, inv;
+#pragma unroll
+        for (int J = 1; J < 4; ++J)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[r] = fmaxf(m[r], tm[J][16 * I + 4 * g + r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float x;
+            s[r] = scale_to(m[r], 10, x);
+            inv[r] = x;
+        }
+        store_tile(t[I], s, I, wave, out.T);
+        if (I == wave && j == 0) *reinterpret_cast<floatx4 *>(&out.m.rt[16 * I + 4 * g]) = inv;
+    }
 }
 
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
-    __shared__ float M[kC][LD], Px[kC][LD], D[kC][LD], X[kC][20], F[4][kC], ga[kC];
-    __shared__ PrepShared sh;
+    constexpr int KS = DK / 32;
+    __shared__ union {
+        float M[kC][LD];
+        Row8<BF16> rows[4][KS][64];  // K as operands, until M is written
+    } big;
+    __shared__ __align__(16) float X[kC][20], tm[4][kC], pre[kC], suf[kC], ga[kC], be[kC];
     const SeqArgs &s = A.s;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
     int b, first;
     const int n = chunk_of_slot(s, blockIdx.x, b, first);
     if (n == 0) return;
     ChunkPrep &out = A.prep[(size_t)blockIdx.x * s.H + h];
-    row_scales<DK, BF16>(s, h, first, n, out.m, sh);
-    if (tid < kC) ga[tid] = tid < n ? s.a[(size_t)(first + tid) * s.H + h] : 1.f;
-    __syncthreads();
-    {  // D inside 16-row blocks; F: the factor from j's block to block I
-        const int j = lane, I = wave;
-        if (I >= j >> 4) {
-            float run = 1.f;
+    Rows<DK, BF16> x;
+    x.load(s, h, first, n);
+    // gates of all 64 tokens, one a lane
+    const size_t tok = (size_t)(first + min(lane, n - 1)) * s.H + h;
+    const float a = lane < n ? s.a[tok] : 1.f, beta = lane < n ? s.beta[tok] : 0.f;
+    float p = a, f = dpp<kShl + 1>(a, 1.f);
+    p *= dpp<kShr + 1>(p, 1.f);
+    p *= dpp<kShr + 2>(p, 1.f);
+    p *= dpp<kShr + 4>(p, 1.f);
+    p *= dpp<kShr + 8>(p, 1.f);
+    f *= dpp<kShl + 1>(f, 1.f);
+    f *= dpp<kShl + 2>(f, 1.f);
+    f *= dpp<kShl + 4>(f, 1.f);
+    f *= dpp<kShl + 8>(f, 1.f);
+    float B[4];                      // products of the blocks
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (16 * I + i > j) run *= ga[16 * I + i];
-                D[16 * I + i][j] = run;
-            }
-        }
-        __syncthreads();
-        float f = 1.f;
-        for (int m = j >> 4; m < I; ++m) f *= D[16 * m + 15][j];
-        F[I][j] = f;
+    for (int i = 0; i < 4; ++i)
+        B[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), 16 * i + 15));
+    if (wave == 0) {
+        pre[lane] = p;
+        suf[lane] = f;
+        ga[lane] = a;
+        be[lane] = beta;
     }
+    x.scales();
+#pragma unroll
+    for (int i = 0; i < KS; ++i) big.rows[wave][i][lane] = x.k[i];
+    const int row = 16 * wave + c16;
     __syncthreads();
-    if (tid < kC) {
-        const float G = ga[0] * D[tid][0] * F[tid >> 4][0];
-        out.m.rk[tid] = sh.ik[tid] * G;
-        out.m.rq[tid] = sh.iq[tid] * G;
-        out.m.rw[tid] = sh.ik[tid] * D[kC - 1][tid] * F[3][tid];
+    if (g == 0) {
+        const float G = (wave > 0 ? B[0] : 1.f) * (wave > 1 ? B[1] : 1.f) * (wave > 2 ? B[2] : 1.f) * pre[row];
+        const float E = (wave < 1 ? B[1] : 1.f) * (wave < 2 ? B[2] : 1.f) * (wave < 3 ? B[3] : 1.f) * suf[row];
+        out.m.sk[row] = x.sk;
+        out.m.sq[row] = x.sq;
+        out.m.rk[row] = x.ik * G;
+        out.m.rq[row] = x.iq * G;
+        out.m.rw[row] = x.ik * E;
     }
-    if (tid < 128) out.m.dec[tid] = ga[0] * D[kC - 1][0] * F[3][0];
+    if (tid < 128) out.m.dec[tid] = B[0] * B[1] * B[2] * B[3];
 
-    const int r16 = lane & 15, g = lane >> 4;
+    floatx4 aa[4], pp[4];
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-        if (ct > (wave | 1)) continue;
-        floatx4 aa = {0.f, 0.f, 0.f, 0.f}, pp = aa;
-        if (ct <= wave) {
+    for (int J = 0; J < 4; ++J) {
+        aa[J] = pp[J] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (J > wave) continue;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            const Row8<BF16> y = big.rows[J][i][lane];
             if constexpr (BF16) {
-#pragma unroll
-                for (int c = 0; c < DK; c += 32) {
-                    const bf16x8 kr = frag_bf16<DK>(s.k, s, h, first, n, 16 * wave + r16, c + 8 * g);
-                    const bf16x8 qr = frag_bf16<DK>(s.q, s, h, first, n, 16 * wave + r16, c + 8 * g);
-                    const bf16x8 kc = frag_bf16<DK>(s.k, s, h, first, n, 16 * ct + r16, c + 8 * g);
-                    aa = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr, kc, aa, 0, 0, 0);
-                    pp = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qr, kc, pp, 0, 0, 0);
-                }
+                const bf16x8 kr = __builtin_bit_cast(bf16x8, x.k[i].w), qr = __builtin_bit_cast(bf16x8, x.q[i].w);
+                const bf16x8 kc = __builtin_bit_cast(bf16x8, y.w);
+                aa[J] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr, kc, aa[J], 0, 0, 0);
+                pp[J] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qr, kc, pp[J], 0, 0, 0);
             } else {
 #pragma unroll
-                for (int c = 0; c < DK; c += 16) {
-                    const float4 kr = frag_f32<DK>(s.k, s, h, first, n, 16 * wave + r16, c + 4 * g);
-                    const float4 qr = frag_f32<DK>(s.q, s, h, first, n, 16 * wave + r16, c + 4 * g);
-                    const float4 kc = frag_f32<DK>(s.k, s, h, first, n, 16 * ct + r16, c + 4 * g);
-                    aa = mfma_f32(kr.x, kc.x, aa);
-                    aa = mfma_f32(kr.y, kc.y, aa);
-                    aa = mfma_f32(kr.z, kc.z, aa);
-                    aa = mfma_f32(kr.w, kc.w, aa);
-                    pp = mfma_f32(qr.x, kc.x, pp);
-                    pp = mfma_f32(qr.y, kc.y, pp);
-                    pp = mfma_f32(qr.z, kc.z, pp);
-                    pp = mfma_f32(qr.w, kc.w, pp);
+                for (int e = 0; e < 8; ++e) {
+                    aa[J] = mfma_f32(x.k[i].get(e), y.get(e), aa[J]);
+                    pp[J] = mfma_f32(x.q[i].get(e), y.get(e), pp[J]);
                 }
             }
         }
+    }
+    const floatx4 pi = four(&pre[16 * wave + 4 * g]), bi = four(&be[16 * wave + 4 * g]);
+    floatx4 dd;                      // decay inside the diagonal block
+    {
+        float run = 1.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * wave + 4 * g + r, j = 16 * ct + r16;
-            const float d = i >= j ? D[i][j] * F[wave][j] : 0.f;
-            M[i][j] = i > j ? sh.be[i] * (aa[r] * d) : 0.f;
-            Px[i][j] = i >= j ? pp[r] * d : 0.f;
+        for (int i = 0; i < 16; ++i) {
+            run *= i > c16 ? ga[16 * wave + i] : 1.f;
+            dd[i & 3] = i >> 2 == g ? run : i < 4 ? 1.f : dd[i & 3];
         }
     }
     __syncthreads();
-    finish(M, Px, D, X, sh.be, out);
-}
-
-// Rows of an operand times the factors of a level, from LDS.
-template <int L>
-__device__ inline float4 row_times(const float (*x)[L], const float (*f)[L], int row, int c) {
-    const float4 a = *reinterpret_cast<const float4 *>(&x[row][c]);
-    const float4 b = *reinterpret_cast<const float4 *>(&f[row][c]);
-    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
-
-template <int DK, int L>
-__device__ inline floatx4 block_product(const float (*x)[L], const float (*k)[L], const float (*f)[L], int I, int J) {
-    const int r16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < DK; c += 16) {
-        const float4 a = row_times<L>(x, f, 16 * I + r16, c + 4 * g);
-        const float4 b = row_times<L>(k, f, 16 * J + r16, c + 4 * g);
-        acc = mfma_f32(a.x, b.x, acc);
-        acc = mfma_f32(a.y, b.y, acc);
-        acc = mfma_f32(a.z, b.z, acc);
-        acc = mfma_f32(a.w, b.w, acc);
+    for (int J = 0; J < 4; ++J) {
+        if (J > wave) continue;
+        float sj = suf[16 * J + c16];
+#pragma unroll
+        for (int m = 1; m < 3; ++m) sj *= m > J && m < wave ? B[m] : 1.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * g + r;
+            const float d = J < wave ? pi[r] * sj : i >= c16 ? dd[r] : 0.f;
+            big.M[16 * wave + i][16 * J + c16] = J < wave || i > c16 ? bi[r] * (aa[J][r] * d) : 0.f;
+            pp[J][r] = J < wave || i >= c16 ? pp[J][r] * d : 0.f;
+        }
     }
-    return acc;
+    store_p(pp, out);
+    __syncthreads();
+    store_t(big.M, X, tm, be, out);
+}
+
+// x s of eight channels as fp16 pairs
+__device__ inline void split8(const float (&x)[8], float s, half8 &hi, half8 &lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        _Float16 a, b;
+        split(x[e], s, a, b);
+        hi[e] = a;
+        lo[e] = b;
+    }
+}
+__device__ inline floatx4 mfma_pairs(half8 ah, half8 al, half8 bh, half8 bl, floatx4 c) {
+    c = mfma16(ah, bh, c);
+    c = mfma16(ah, bl, c);
+    return mfma16(al, bh, c);
 }
 
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
-    constexpr int L = DK + 4, G4 = 256 / DK;  // G4 groups of DK threads
-    __shared__ float K[kC][L], Q[kC][L], Ga[kC][L], F[kC][L], dg[2][4][16][17];
-    __shared__ PrepShared sh;
+    constexpr int KS = DK / 32;
+    __shared__ union {
+        float M[kC][LD];
+        float g[2][kC / 4][DK];      // products up to and after each four rows of a block, until M is written
+    } big;
+    __shared__ half8 Y[3][KS][2][64];  // k suf of waves 0 to 2
+    __shared__ __align__(16) float X[kC][20], tm[4][kC], dp[4][16][20], ik[kC], iq[kC], be[kC];
     const SeqArgs &s = A.s;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
     int b, first;
     const int n = chunk_of_slot(s, blockIdx.x, b, first);
     if (n == 0) return;
     ChunkPrep &out = A.prep[(size_t)blockIdx.x * s.H + h];
-    row_scales<DK, BF16>(s, h, first, n, out.m, sh);
-    for (int i = tid; i < kC * (DK / 4); i += 256) {
-        const int row = i / (DK / 4), c = i % (DK / 4) * 4;
-        float k[4] = {}, q[4] = {}, a[4] = {1.f, 1.f, 1.f, 1.f};
-        if (row < n) {
-            const size_t at = ((size_t)(first + row) * s.H + h) * DK + c;
-            load_row<BF16>(s.k, at, k);
-            load_row<BF16>(s.q, at, q);
-            load_f32(s.a + at, a);
+    Rows<DK, BF16> x;
+    x.load(s, h, first, n);
+    x.scales();
+    const int row = 16 * w + c16;
+    if (g == 0) {
+        ik[row] = x.ik;
+        iq[row] = x.iq;
+        be[row] = row < n ? s.beta[(size_t)(first + row) * s.H + h] : 0.f;
+        out.m.sk[row] = x.sk;
+        out.m.sq[row] = x.sq;
+        out.m.rk[row] = out.m.rw[row] = x.ik;
+        out.m.rq[row] = x.iq;
+    }
+    const bool b1 = c16 & 1, b2 = c16 & 2, b4 = c16 & 4, b8 = c16 & 8, on = row < n;
+    float kp[KS][8], qp[KS][8];      // k pre, q pre
+    floatx4 cut4 = {0.f, 0.f, 0.f, 0.f}, cut8 = cut4;
+    float da[3] = {}, dq[4] = {};    // 4x4 blocks: rows d earlier, A for d = 1, 2, 3 and P for d = 0 .. 3
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        const floatx4 a0 = four(s.a + x.at + 32 * i), a1 = four(s.a + x.at + 32 * i + 4);
+        float z4[8], z8[8], y4[8], y8[8], y16[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = on ? e < 4 ? a0[e & 3] : a1[e & 3] : 1.f, k = x.k[i].get(e), q = x.q[i].get(e);
+            // 4x4 blocks
+            dq[0] = __builtin_fmaf(q, k, dq[0]);
+            float v = dpp<kShr + 1>(k) * a;
+            da[0] = __builtin_fmaf(k, v, da[0]);
+            dq[1] = __builtin_fmaf(q, v, dq[1]);
+            float d = a * dpp<kShr + 1>(a);
+            v = dpp<kShr + 2>(k) * d;
+            da[1] = __builtin_fmaf(k, v, da[1]);
+            dq[2] = __builtin_fmaf(q, v, dq[2]);
+            d *= dpp<kShr + 2>(a);
+            v = dpp<kShr + 3>(k) * d;
+            da[2] = __builtin_fmaf(k, v, da[2]);
+            dq[3] = __builtin_fmaf(q, v, dq[3]);
+            // products within 2, 4, 8 and 16 rows: up to the row (p), after it (f)
+            const float p2 = a * pick(b1, dpp<quad(0, 0, 2, 2)>(a), 1.f);
+            const float p4 = p2 * pick(b2, dpp<quad(1, 1, 1, 1)>(p2), 1.f);
+            const float t4 = dpp<quad(3, 3, 3, 3)>(p4);
+            const float p8 = p4 * pick(b4, dpp<kShr + 4>(t4), 1.f);
+            const float p16 = p8 * pick(b8, dpp<kBcast + 7>(p8), 1.f);
+            float f = pick(b1, 1.f, dpp<quad(1, 1, 3, 3)>(a));
+            f *= pick(b2, 1.f, dpp<quad(3, 3, 3, 3)>(p2));
+            y4[e] = k * f;
+            f *= pick(b4, 1.f, dpp<kShl + 4>(t4));
+            y8[e] = k * f;
+            f *= pick(b8, 1.f, dpp<kBcast + 15>(p8));
+            y16[e] = k * f;
+            // the later half's rows of K, and of Q in the rows that the earlier half leaves free
+            z4[e] = pick(b4, k * p4 * x.sk, dpp<kShl + 4>(q * p4 * x.sq));
+            z8[e] = pick(b8, k * p8 * x.sk, dpp<kShl + 8>(q * p8 * x.sq));
+            kp[i][e] = k * p16;
+            qp[i][e] = q * p16;
+            if ((c16 & 3) == 3) {
+                big.g[0][row >> 2][32 * i + 8 * g + e] = p16;
+                big.g[1][row >> 2][32 * i + 8 * g + e] = f;
+            }
         }
-        *reinterpret_cast<float4 *>(&K[row][c]) = make_float4(k[0], k[1], k[2], k[3]);
-        *reinterpret_cast<float4 *>(&Q[row][c]) = make_float4(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<float4 *>(&Ga[row][c]) = make_float4(a[0], a[1], a[2], a[3]);
+        half8 zh, zl, yh, yl;
+        split8(z4, 1.f, zh, zl);
+        split8(y4, x.sk, yh, yl);
+        cut4 = mfma_pairs(zh, zl, yh, yl, cut4);
+        split8(z8, 1.f, zh, zl);
+        split8(y8, x.sk, yh, yl);
+        cut8 = mfma_pairs(zh, zl, yh, yl, cut8);
+        if (w < 3) {
+            split8(y16, x.sk, yh, yl);
+            Y[w][i][0][lane] = yh;
+            Y[w][i][1][lane] = yl;
+        }
     }
     __syncthreads();
-    if (tid < kC) {
-        out.m.rk[tid] = sh.ik[tid];
-        out.m.rq[tid] = sh.iq[tid];
-        out.m.rw[tid] = sh.ik[tid];
-    }
-    {  // gate products before and after each four tokens
+    // gate products of the whole chunk before and after each four tokens
+    {
         ChunkGates &o = A.gates[(size_t)blockIdx.x * s.H + h];
         const int c = tid % DK;
-        float run = 1.f;
-        if (tid < DK) {
-#pragma unroll 16
-            for (int i = 0; i < kC; ++i) {
-                if (i % 4 == 0) o.pre[i / 4][c] = run;
-                run *= Ga[i][c];
-            }
-        } else if (tid < 2 * DK) {
-#pragma unroll 16
-            for (int i = kC - 1; i >= 0; --i) {
-                if (i % 4 == 3) o.suf[i / 4][c] = run;
-                run *= Ga[i][c];
-            }
-        }
-    }
-    // splits at 16 and 48: rows of blocks 0 and 2 carry the product up to the
-    // block's end, rows of blocks 1 and 3 the product from the block's start
-    const int c = tid % DK, grp = tid / DK;
-    for (int blk = grp; blk < 4; blk += G4) {
-        float run = 1.f;
-        if (blk & 1) {
-            for (int i = 16 * blk; i < 16 * blk + 16; ++i) {
-                run *= Ga[i][c];
-                F[i][c] = run;
-            }
-        } else {
-            for (int i = 16 * blk + 15; i >= 16 * blk; --i) {
-                F[i][c] = run;
-                run *= Ga[i][c];
-            }
-        }
-    }
-    __syncthreads();
-    const int pair = wave & 1;  // blocks (1, 0) and (3, 2); A by waves 0 and 1, P by 2 and 3
-    const floatx4 near = block_product<DK, L>(wave < 2 ? K : Q, K, F, 2 * pair + 1, 2 * pair);
-    __syncthreads();
-    // split at 32
-    if (grp == 0) {
-        float run = 1.f;
-        for (int i = 31; i >= 0; --i) {
-            F[i][c] = run;
-            run *= Ga[i][c];
-        }
-    } else if (grp == 1) {
-        float run = 1.f;
-        for (int i = 32; i < kC; ++i) {
-            run *= Ga[i][c];
-            F[i][c] = run;
-        }
-    }
-    __syncthreads();
-    const int fi = 2 + (wave & 1), fj = wave >> 1;
-    const floatx4 farA = block_product<DK, L>(K, K, F, fi, fj);
-    const floatx4 farP = block_product<DK, L>(Q, K, F, fi, fj);
-    if (tid < DK) out.m.dec[tid] = F[0][tid] * Ga[0][tid] * F[kC - 1][tid];
-    // diagonal block `wave`: lane (j, g) follows k_j over the channels of group g
-    const int j = lane & 15, g = lane >> 4;
-    {
-        constexpr int W = DK / 4;
-        float w[W];
-        const int row0 = 16 * wave;
+        float B[4];
 #pragma unroll
-        for (int x = 0; x < W; x += 4) {
-            const float4 k = *reinterpret_cast<const float4 *>(&K[row0 + j][W * g + x]);
-            w[x] = k.x;
-            w[x + 1] = k.y;
-            w[x + 2] = k.z;
-            w[x + 3] = k.w;
-        }
-        for (int i = 0; i < 16; ++i) {
-            float da = 0.f, dp = 0.f;
-            const bool on = i > j;
+        for (int i = 0; i < 4; ++i) B[i] = big.g[0][4 * i + 3][c];
 #pragma unroll
-            for (int x = 0; x < W; x += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&Ga[row0 + i][W * g + x]);
-                const float4 k = *reinterpret_cast<const float4 *>(&K[row0 + i][W * g + x]);
-                const float4 q = *reinterpret_cast<const float4 *>(&Q[row0 + i][W * g + x]);
-                w[x] *= on ? a.x : 1.f;
-                w[x + 1] *= on ? a.y : 1.f;
-                w[x + 2] *= on ? a.z : 1.f;
-                w[x + 3] *= on ? a.w : 1.f;
-                da = __builtin_fmaf(k.x, w[x], da);
-                da = __builtin_fmaf(k.y, w[x + 1], da);
-                da = __builtin_fmaf(k.z, w[x + 2], da);
-                da = __builtin_fmaf(k.w, w[x + 3], da);
-                dp = __builtin_fmaf(q.x, w[x], dp);
-                dp = __builtin_fmaf(q.y, w[x + 1], dp);
-                dp = __builtin_fmaf(q.z, w[x + 2], dp);
-                dp = __builtin_fmaf(q.w, w[x + 3], dp);
+        for (int i = 0; i < 16 * DK / 256; ++i) {
+            const int q4 = tid / DK + 256 / DK * i, blk = q4 >> 2;
+            float u = q4 & 3 ? big.g[0][q4 - 1][c] : 1.f, v = big.g[1][q4][c];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                u *= m < blk ? B[m] : 1.f;
+                v *= m > blk ? B[m] : 1.f;
             }
-            da += __shfl_xor(da, 16);
-            da += __shfl_xor(da, 32);
-            dp += __shfl_xor(dp, 16);
-            dp += __shfl_xor(dp, 32);
-            if (g == 0) {
-                dg[0][wave][i][j] = on ? da : 0.f;
-                dg[1][wave][i][j] = i >= j ? dp : 0.f;
+            o.pre[q4][c] = u;
+            o.suf[q4][c] = v;
+        }
+        if (tid < DK) out.m.dec[c] = B[0] * B[1] * B[2] * B[3];
+    }
+    floatx4 aa[4], pp[4];
+#pragma unroll
+    for (int J = 2; J >= 0; --J) {
+        aa[J] = pp[J] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (J >= w) continue;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (J < w - 1) {         // the block between, J + 1, comes in
+                const float *m = &big.g[0][4 * J + 7][32 * i + 8 * g];
+                const floatx4 m0 = four(m), m1 = four(m + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    kp[i][e] *= e < 4 ? m0[e & 3] : m1[e & 3];
+                    qp[i][e] *= e < 4 ? m0[e & 3] : m1[e & 3];
+                }
             }
+            const half8 yh = Y[J][i][0][lane], yl = Y[J][i][1][lane];
+            half8 zh, zl;
+            split8(kp[i], x.sk, zh, zl);
+            aa[J] = mfma_pairs(zh, zl, yh, yl, aa[J]);
+            split8(qp[i], x.sq, zh, zl);
+            pp[J] = mfma_pairs(zh, zl, yh, yl, pp[J]);
         }
     }
     __syncthreads();
-    // K, Q, Ga and F are done with: M, P, T and X take their places
-    static_assert(sizeof(K) >= sizeof(float) * kC * LD, "a 64x64 matrix fits");
-    float(*M)[LD] = reinterpret_cast<float(*)[LD]>(&K[0][0]);
-    float(*Px)[LD] = reinterpret_cast<float(*)[LD]>(&Q[0][0]);
-    float(*Tx)[LD] = reinterpret_cast<float(*)[LD]>(&Ga[0][0]);
-    float(*X)[20] = reinterpret_cast<float(*)[20]>(&F[0][0]);
+    const floatx4 bi = four(&be[16 * w + 4 * g]), iki = four(&ik[16 * w + 4 * g]), iqi = four(&iq[16 * w + 4 * g]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i1 = 16 * (2 * pair + 1) + 4 * g + r, j1 = 16 * (2 * pair) + j;
-        if (wave < 2) M[i1][j1] = sh.be[i1] * near[r];
-        else Px[i1][j1] = near[r];
-        const int i2 = 16 * fi + 4 * g + r, j2 = 16 * fj + j;
-        M[i2][j2] = sh.be[i2] * farA[r];
-        Px[i2][j2] = farP[r];
-        const int i3 = 16 * wave + 4 * g + r;
-        M[i3][16 * wave + j] = sh.be[i3] * dg[0][wave][4 * g + r][j];
-        Px[i3][16 * wave + j] = dg[1][wave][4 * g + r][j];
-        if (!(wave & 1)) {  // the block right of an even diagonal block
-            M[i3][16 * wave + 16 + j] = 0.f;
-            Px[i3][16 * wave + 16 + j] = 0.f;
+    for (int J = 0; J < 3; ++J) {
+        if (J >= w) continue;
+        const float ikj = ik[16 * J + c16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            big.M[16 * w + 4 * g + r][16 * J + c16] = bi[r] * (aa[J][r] * iki[r] * ikj);
+            pp[J][r] = pp[J][r] * iqi[r] * ikj;
+        }
+    }
+    // the diagonal block, from its cuts
+    float(*Md)[LD] = reinterpret_cast<float(*)[LD]>(&big.M[16 * w][16 * w]);
+    const bool both = g & 1;         // cut 4: groups 1 and 3 hold A of rows 4 g .., 0 and 2 P of rows 4 g + 4 ..
+    if (g < 2 ? c16 < 4 : c16 >= 8 && c16 < 12) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * (g | 1) + r;
+            if (both) Md[i][c16] = be[16 * w + i] * (cut4[r] * ik[16 * w + i] * x.ik);
+            else dp[w][i][c16] = cut4[r] * iq[16 * w + i] * x.ik;
+        }
+    }
+    if (c16 < 8) {                   // cut 8: groups 2 and 3 A of rows 4 g .., 0 and 1 P of rows 4 g + 8 ..
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * (g | 2) + r;
+            if (g & 2) Md[i][c16] = be[16 * w + i] * (cut8[r] * ik[16 * w + i] * x.ik);
+            else dp[w][i][c16] = cut8[r] * iq[16 * w + i] * x.ik;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float p = sum_groups(dq[d]), m = sum_groups(d ? da[d - 1] : 0.f);
+        if (g == 0 && (c16 & 3) >= d) {
+            dp[w][c16][c16 - d] = p;
+            Md[c16][c16 - d] = d ? be[row] * m : 0.f;
         }
     }
     __syncthreads();
-    finish(M, Px, Tx, X, sh.be, out);
+#pragma unroll
+    for (int J = 0; J < 4; ++J)
+        if (J == w)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pp[J][r] = 4 * g + r >= c16 ? dp[w][4 * g + r][c16] : 0.f;
+    store_p(pp, out);
+    store_t(big.M, X, tm, be, out);
 }
 
 }  // namespace
