@@ -317,8 +317,8 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
  * Allocates nothing, does not synchronize, may be captured in a HIP graph.  A
  * workspace must not be used by two calls that overlap in time.
  * Errors: STQ_ERR_INVALID (NULL, B or N negative, a bad rule),
- * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, B > 65535), STQ_ERR_TOO_SMALL,
- * STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, more than 2^31 chunks times
+ * heads), STQ_ERR_TOO_SMALL, STQ_ERR_ALIGN, STQ_ERR_DEVICE.
  */
 stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
                              const void *d_q, const void *d_k, const void *d_v, const float *d_a,

@@ -59,7 +59,10 @@ struct ChunkArgs {
     ChunkPrep *prep;                 // [chunk slots][H]
     ChunkGates *gates;               // the same, key-vector gates only
     int32_t slots;                   // chunk slots: N / 64 + B
+    int32_t *order;                  // [B] sequences, longest first, or nullptr: as they come
 };
+
+constexpr int kOrdered = 1024;       // sequences that are put in order of length
 
 // Chunk c of sequence b (first token t0) has slot t0 / 64 + b + c: slots of
 // different chunks differ, and none reaches N / 64 + B.
@@ -78,6 +81,23 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 // A wave's number in its workgroup, in a scalar register: branches on it are the whole
 // wave's (matrix instructions write their results whatever lanes are on).
 __device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Workgroup `id` of a line of groups of `m` (the heads of a sequence or chunk):
+// its group and its place in it.  Workgroups go to the eight XCDs in turn.  A head's rows
+// lie H d elements apart, often a multiple of the L2's channel interleave, so a head stays in
+// one or two channels: with heads dealt out in turn an XCD would only see heads, and
+// channels, a multiple of 8 apart.  Here it takes m / 8 neighbouring heads of every
+// group, other ones in the next group.
+__device__ inline void xcd_place(uint32_t id, uint32_t m, uint32_t &group, uint32_t &at) {
+    if (m & 7) {
+        group = id / m;
+        at = id % m;
+        return;
+    }
+    const uint32_t each = m >> 3, xcd = id & 7, i = id >> 3;
+    group = i / each;
+    at = ((xcd + group) & 7) * each + i % each;
+}
 
 // The chunk of slot x: its sequence, first token and number of tokens; 0 tokens
 // where the slot holds none.  Called by whole waves: the sequence is searched for 64

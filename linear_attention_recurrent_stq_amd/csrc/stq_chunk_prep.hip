@@ -216,6 +216,22 @@ __device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)
     }
 }
 
+// The sequences by length, longest first (one workgroup): the pass of the state takes as
+// long as its last sequence to end, and few sequences fill the chip at a time.
+__device__ inline void order_sequences(const ChunkArgs &A, int *len) {
+    for (int b = threadIdx.x; b < A.s.B; b += 256) {
+        int t0, t1;
+        seq_range(A.s, b, t0, t1);
+        len[b] = t1 - t0;
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < A.s.B; b += 256) {
+        int at = 0;
+        for (int i = 0; i < A.s.B; ++i) at += len[i] > len[b] || (len[i] == len[b] && i < b);
+        A.order[at] = b;
+    }
+}
+
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     constexpr int KS = DK / 32;
@@ -225,11 +241,15 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     } big;
     __shared__ __align__(16) float X[kC][20], tm[4][kC], pre[kC], suf[kC], ga[kC], be[kC];
     const SeqArgs &s = A.s;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
+    static_assert(sizeof(X) >= kOrdered * sizeof(int), "the lengths fit");
+    if (blockIdx.x == (uint32_t)A.slots * (uint32_t)s.H) return order_sequences(A, reinterpret_cast<int *>(&X[0][0]));
+    uint32_t slot, h;
+    xcd_place(blockIdx.x, s.H, slot, h);
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
     int b, first;
-    const int n = chunk_of_slot(s, blockIdx.x, b, first);
+    const int n = chunk_of_slot(s, slot, b, first);
     if (n == 0) return;
-    ChunkPrep &out = A.prep[(size_t)blockIdx.x * s.H + h];
+    ChunkPrep &out = A.prep[(size_t)slot * s.H + h];
     Rows<DK, BF16> x;
     x.load(s, h, first, n);
     // gates of all 64 tokens, one a lane
@@ -348,11 +368,15 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
     __shared__ half8 Y[3][KS][2][64];  // k suf of waves 0 to 2
     __shared__ __align__(16) float X[kC][20], tm[4][kC], dp[4][16][20], ik[kC], iq[kC], be[kC];
     const SeqArgs &s = A.s;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
+    static_assert(sizeof(X) >= kOrdered * sizeof(int), "the lengths fit");
+    if (blockIdx.x == (uint32_t)A.slots * (uint32_t)s.H) return order_sequences(A, reinterpret_cast<int *>(&X[0][0]));
+    uint32_t slot, h;
+    xcd_place(blockIdx.x, s.H, slot, h);
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
     int b, first;
-    const int n = chunk_of_slot(s, blockIdx.x, b, first);
+    const int n = chunk_of_slot(s, slot, b, first);
     if (n == 0) return;
-    ChunkPrep &out = A.prep[(size_t)blockIdx.x * s.H + h];
+    ChunkPrep &out = A.prep[(size_t)slot * s.H + h];
     Rows<DK, BF16> x;
     x.load(s, h, first, n);
     x.scales();
@@ -430,7 +454,7 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
     __syncthreads();
     // gate products of the whole chunk before and after each four tokens
     {
-        ChunkGates &o = A.gates[(size_t)blockIdx.x * s.H + h];
+        ChunkGates &o = A.gates[(size_t)slot * s.H + h];
         const int c = tid % DK;
         float B[4];
 #pragma unroll
@@ -526,7 +550,7 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
 }  // namespace
 
 hipError_t launch_chunk_prep(const ChunkArgs &a, int dk, bool keyvec, bool bf16, hipStream_t s) {
-    const dim3 grid((unsigned)a.slots, (unsigned)a.s.H);
+    const dim3 grid((unsigned)a.slots * (unsigned)a.s.H + (a.order ? 1u : 0u));
     if (keyvec) {
         if (dk == 64 && bf16) k_prep_keyvec<64, true><<<grid, 256, 0, s>>>(a);
         else if (dk == 64) k_prep_keyvec<64, false><<<grid, 256, 0, s>>>(a);

@@ -39,7 +39,7 @@ stq_status check_rule(const stq_rule *r) {
 
 stq_status check_sizes(const stq_rule *r, int32_t B, int32_t N) {
     if (B < 0 || N < 0) return fail(STQ_ERR_INVALID, "B and N must be >= 0");
-    if ((int64_t)B * r->H > INT32_MAX) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^31 - 1");
+    if ((int64_t)B * r->H * 2 > INT32_MAX) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^30");
     return STQ_OK;
 }
 
@@ -126,7 +126,9 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
     if (backward) return fail(STQ_ERR_UNSUPPORTED, "no backward pass");
     size_t each = sizeof(stq::ChunkPrep);
     if (rule->gate == STQ_GATE_KEYVEC) each += sizeof(stq::ChunkGates);
-    *bytes = each * (size_t)stq::chunk_slots(N, B) * rule->H;
+    if (((int64_t)N / stq::kC + B) * rule->H > INT32_MAX)
+        return fail(STQ_ERR_UNSUPPORTED, "too many chunks for one call");
+    *bytes = each * (size_t)stq::chunk_slots(N, B) * rule->H + sizeof(int32_t) * stq::kOrdered;
     return STQ_OK;
 }
 
@@ -136,7 +138,6 @@ stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const i
                              void *d_workspace, size_t workspace_bytes, void *stream) {
     size_t need = 0;
     if (stq_status s = stq_chunk_workspace(rule, B, N, 0, &need)) return s;
-    if (B > 65535) return fail(STQ_ERR_UNSUPPORTED, "B exceeds 65535");
     if (B == 0) return STQ_OK;
     if (stq_status s = check_ints(d_cu_seqlens, true, "cu_seqlens")) return s;
     if (N > 0)  // without tokens the states are passed on and nothing else is touched
@@ -150,14 +151,14 @@ stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const i
     a.initial = d_initial;
     a.last = d_final;
     a.o = d_o;
-    a.prep = static_cast<stq::ChunkPrep *>(d_workspace);
     a.slots = stq::chunk_slots(N, B);
+    if (B > 1 && B <= stq::kOrdered) a.order = static_cast<int32_t *>(d_workspace);
+    a.prep = reinterpret_cast<stq::ChunkPrep *>(static_cast<int32_t *>(d_workspace) + stq::kOrdered);
     a.gates = reinterpret_cast<stq::ChunkGates *>(a.prep + (size_t)a.slots * rule->H);
     const bool keyvec = rule->gate == STQ_GATE_KEYVEC, bf16 = rule->io_dtype == STQ_BF16;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (N > 0)
-        if (stq_status s = launched(stq::launch_chunk_prep(a, rule->d_k, keyvec, bf16, st), "chunk preparation"))
-            return s;
+    if (stq_status s = launched(stq::launch_chunk_prep(a, rule->d_k, keyvec, bf16, st), "chunk preparation"))
+        return s;
     return launched(stq::launch_chunk_forward(a, rule->d_k, rule->d_v, keyvec, bf16, st), "chunk forward");
 }
 
