@@ -325,6 +325,28 @@ stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const i
                              const float *d_beta, const float *d_initial, void *d_o, float *d_final,
                              void *d_workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Gradients of a scalar loss through stq_chunk_forward, from the gradients of its
+ * outputs; the states along the way are formed anew from the inputs.
+ *   d_initial as given to the forward pass (NULL: zero)
+ *   d_do      [N,H,d_v] io_dtype, gradient of o
+ *   d_dfinal  [B,H,d_k,d_v] fp32, gradient of the final states, NULL: zero
+ *   d_dq, d_dk [N,H,d_k], d_dv [N,H,d_v] io_dtype; d_da as a, d_dbeta as beta,
+ *             fp32; d_dinitial [B,H,d_k,d_v] fp32, NULL: not wanted; may be
+ *             d_dfinal.  Outputs of tokens outside every sequence keep what they held.
+ * The gradient of a gate a is formed as that of its logarithm (a times it: sums in
+ * fp32) over a, so it is exact to rounding where the gates are of ordinary size;
+ * its error grows as 1/a, and where a is 0 it is given as 0.
+ * A workspace of stq_chunk_workspace(backward = 1); everything else, and the
+ * errors, as for stq_chunk_forward.
+ */
+stq_status stq_chunk_backward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
+                              const void *d_q, const void *d_k, const void *d_v, const float *d_a,
+                              const float *d_beta, const float *d_initial, const void *d_do,
+                              const float *d_dfinal, void *d_dq, void *d_dk, void *d_dv, float *d_da,
+                              float *d_dbeta, float *d_dinitial, void *d_workspace,
+                              size_t workspace_bytes, void *stream);
+
 /* Bytes of device workspace that stq_verify_draft needs for B requests over a
  * vocabulary of V tokens. */
 stq_status stq_verify_workspace(int32_t B, int32_t V, size_t *bytes);

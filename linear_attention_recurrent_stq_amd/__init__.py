@@ -7,7 +7,8 @@ built; there is no fallback.
 
 Names follow the C ABI in ``include/stq.h``: ``Layout`` (stq_pack_layout),
 ``Pool`` (stq_alloc_pool), ``decode_step``, ``unpack``, ``pack``; over several
-tokens of each sequence: ``chunk_forward``, ``recurrent_step``, ``verify_draft``.
+tokens of each sequence: ``chunk_forward``, ``chunk_backward``,
+``recurrent_step``, ``verify_draft``.
 """
 from __future__ import annotations
 
@@ -38,7 +39,7 @@ SYMBOLS = ["stq_status_string", "stq_last_error", "stq_pack_layout", "stq_layout
            "stq_layout_head", "stq_layout_free", "stq_alloc_pool", "stq_decode_step",
            "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids", "stq_allocate_bits",
            "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft", "stq_chunk_workspace",
-           "stq_chunk_forward"]
+           "stq_chunk_forward", "stq_chunk_backward"]
 
 
 class StqConfig(C.Structure):
@@ -80,12 +81,13 @@ _lib.stq_fit_scales.argtypes = [C.POINTER(StqPool), C.c_int32, _P, _P]
 _lib.stq_recurrent_step.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 7 + [_I] + [_P] * 4
 _lib.stq_chunk_workspace.argtypes = [C.POINTER(StqRule), _I, _I, _I, C.POINTER(C.c_size_t)]
 _lib.stq_chunk_forward.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 10 + [C.c_size_t, _P]
+_lib.stq_chunk_backward.argtypes = [C.POINTER(StqRule), _I, _I] + [_P] * 16 + [C.c_size_t, _P]
 _lib.stq_verify_workspace.argtypes = [_I, _I, C.POINTER(C.c_size_t)]
 _lib.stq_verify_draft.argtypes = [_I] * 4 + [_P] * 8 + [C.c_size_t, _P]
 for _f in ("stq_pack_layout", "stq_layout_query", "stq_layout_head", "stq_alloc_pool",
            "stq_decode_step", "stq_unpack", "stq_pack", "stq_fit_scales", "stq_check_slot_ids",
            "stq_allocate_bits", "stq_recurrent_step", "stq_verify_workspace", "stq_verify_draft",
-           "stq_chunk_workspace", "stq_chunk_forward"):
+           "stq_chunk_workspace", "stq_chunk_forward", "stq_chunk_backward"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -438,6 +440,31 @@ def chunk_forward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, o, *, initial_s
             C.byref(plan.rule), B, N, *ptrs, first, _dptr(o, "o", v.dtype), last,
             C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
             "stq_chunk_forward")
+
+
+def chunk_backward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, do, dq, dk, dv, da, dbeta, *,
+                   initial_state=None, d_final_state=None, d_initial_state=None, stream=None) -> None:
+    """stq_chunk_backward on torch device tensors: from the gradients do [N,H,d_v]
+    (as v) and d_final_state of chunk_forward's outputs, those of its inputs, each of its
+    input's shape and type.  The plan needs backward=True."""
+    import torch
+    if not plan.backward:
+        raise ValueError("the plan has no room for the backward pass (backward=True)")
+    B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
+    outs = []
+    for t, like, what in ((do, v, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (da, a, "da"),
+                          (dbeta, beta, "dbeta")):
+        if t.shape != like.shape:
+            raise ValueError(f"{what} must be {tuple(like.shape)}")
+        outs.append(_dptr(t, what, like.dtype))
+    _one_device(q, do=do, dq=dq, dk=dk, dv=dv, da=da, dbeta=dbeta)
+    first, dlast, dfirst = plan.states(B, q, initial_state=initial_state, d_final_state=d_final_state,
+                                       d_initial_state=d_initial_state)
+    with torch.cuda.device(q.device):
+        _check(_lib.stq_chunk_backward(
+            C.byref(plan.rule), B, N, *ptrs, first, outs[0], dlast, *outs[1:], dfirst,
+            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
+            "stq_chunk_backward")
 
 
 class VerifyPlan:

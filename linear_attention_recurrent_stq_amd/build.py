@@ -30,7 +30,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = [os.path.join(HERE, "csrc", f)
            for f in ("stq_host.cpp", "stq_seq_host.cpp", "stq_alloc.cpp", "stq_kernels.hip",
                      "stq_window.hip", "stq_recurrent.hip", "stq_verify.hip",
-                     "stq_chunk_prep.hip", "stq_chunk_fwd.hip")]
+                     "stq_chunk_prep.hip", "stq_chunk_fwd.hip", "stq_chunk_rev.hip",
+                     "stq_chunk_grad.hip")]
 VALIDATING = 2  # the first sources: their debug build validates slot ids
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -37,11 +37,19 @@ struct ChunkMeta {
     float rt[kC], rp[kC];            // factors that undo the row scales of T and P
     float rw[kC];                    // factor of u_i in the state's update: 2^-e (and G_64/G_i)
     float dec[128];                  // G_64 per key channel
+    float rn[kC], rpt[kC];           // backward: factors that undo the row scales of N^T and P^T
+    float be[kC];                    // backward: beta, 0 past the last token
 };
 struct ChunkPrep {
     uint16_t T[2][kTri][kFrag];
-    uint16_t P[2][kTri][kFrag];
+    uint16_t P[2][kTri][kFrag];      // backward: A
     ChunkMeta m;
+};
+// The backward pass's other matrices: N^T, N = (I + diag(beta) A)^-1, and P^T, upper
+// triangular, fragments in the order rows 0 (k steps 0, 1), 1 (0, 1), 2 (1), 3 (1).
+struct ChunkBack {
+    uint16_t N[2][kTri][kFrag];
+    uint16_t P[2][kTri][kFrag];
 };
 static_assert(sizeof(ChunkPrep) % 256 == 0, "entries of the workspace stay aligned");
 
@@ -60,6 +68,14 @@ struct ChunkArgs {
     ChunkGates *gates;               // the same, key-vector gates only
     int32_t slots;                   // chunk slots: N / 64 + B
     int32_t *order;                  // [B] sequences, longest first, or nullptr: as they come
+    // The backward pass (back not nullptr): per (chunk, head)
+    ChunkBack *back;
+    float *S, *dS;                   // first state; gradient of the last one [d_k,d_v]
+    float *w, *y;                    // delta errors; gradients of u through N^T [64,d_v]
+    const void *dout;                // [N,H,d_v] io dtype
+    const float *dlast;              // [B,H,d_k,d_v] or nullptr
+    void *dq, *dk, *dv;              // io dtype
+    float *da, *dbeta, *dinitial;    // (dinitial may be nullptr)
 };
 
 constexpr int kOrdered = 1024;       // sequences that are put in order of length
@@ -70,6 +86,9 @@ inline int chunk_slots(int N, int B) { return N / kC + B; }
 
 hipError_t launch_chunk_prep(const ChunkArgs &a, int dk, bool keyvec, bool bf16, hipStream_t s);
 hipError_t launch_chunk_forward(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);
+
+hipError_t launch_chunk_reverse(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);
+hipError_t launch_chunk_grad(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);
 
 #if defined(__HIPCC__)
 
@@ -155,8 +174,68 @@ template <int ctrl>
 __device__ inline float dpp(float x, float old = 0.f) {
     return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), ctrl, 0xf, 0xf, false));
 }
+// The same, 0 where there is none: it folds into the instruction that takes it.
+template <int ctrl>
+__device__ inline float dpp0(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), ctrl, 0xf, 0xf, true));
+}
 constexpr int kShl = 0x100, kShr = 0x110, kRor = 0x120, kBcast = 0x150;  // lane i + n, i - n, i - n mod 16, n
 constexpr int quad(int a, int b, int c, int d) { return a | b << 2 | c << 4 | d << 6; }
+
+// A choice whose both values are formed by every lane: a value read across lanes
+// inside a branch would find the other lanes switched off.
+__device__ inline float pick(bool c, float x, float y) { return c ? x : y; }
+
+// max over the lanes of a row of 16
+__device__ inline float max_row(float x) {
+    x = fmaxf(x, dpp<kRor + 8>(x));
+    x = fmaxf(x, dpp<kRor + 4>(x));
+    x = fmaxf(x, dpp<kRor + 2>(x));
+    return fmaxf(x, dpp<kRor + 1>(x));
+}
+// sum over the lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ inline float sum_groups(float x) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline floatx4 four(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
+
+// Eight consecutive channels as they are in memory.
+template <bool BF16> struct Row8;
+template <> struct Row8<true> {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 w;
+    __device__ void load(const void *p, size_t at) {
+        w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + at);
+    }
+    __device__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+};
+template <> struct Row8<false> {
+    floatx4 x, y;
+    __device__ void load(const void *p, size_t at) {
+        x = four(static_cast<const float *>(p) + at);
+        y = four(static_cast<const float *>(p) + at + 4);
+    }
+    __device__ float get(int i) const { return i < 4 ? x[i] : y[i - 4]; }
+};
+
+// x s of eight channels as fp16 pairs
+__device__ inline void split8(const float (&x)[8], float s, half8 &hi, half8 &lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        _Float16 a, b;
+        split(x[e], s, a, b);
+        hi[e] = a;
+        lo[e] = b;
+    }
+}
+__device__ inline floatx4 mfma_pairs(half8 ah, half8 al, half8 bh, half8 bl, floatx4 c) {
+    c = mfma16(ah, bh, c);
+    c = mfma16(ah, bl, c);
+    return mfma16(al, bh, c);
+}
 
 // x[j] of lane i of a quad becomes x[i] of lane j.
 template <int ctrl>

@@ -1,0 +1,350 @@
+// The passes of the state, or its gradient, through the chunks of a sequence: the producing
+// waves, and what the multiplying waves share.  Device code only.
+#pragma once
+
+#include "stq_chunk.h"
+
+namespace stq {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMeta = sizeof(ChunkMeta) / 16;  // 16-byte pieces
+constexpr int kPart = kTri * kFrag * 2 / 16;   // of T's or P's hi or lo part
+
+// Where lane (row, g)'s eight halves stand in a fragment: rows are permuted so
+// that the producers' writes (fixed row, all g and k steps) and the readers'
+// (fixed k step, all rows) both spread over the banks.
+__device__ inline int place_k(int row16, int g, int ks) { return (g * 16 + (row16 ^ ((4 * g + ks) & 15))) * 8; }
+__device__ inline int place_w(int ch16, int g, int ct) { return (g * 16 + (ch16 ^ (ct & 3))) * 8; }
+
+// Four elements as they are in memory.
+template <bool BF16> struct Raw4;
+template <> struct Raw4<true> { typedef uint2 type; };
+template <> struct Raw4<false> { typedef float4 type; };
+
+__device__ inline void widen(uint2 w, float (&x)[4]) {
+    x[0] = bf16_lo(w.x);
+    x[1] = bf16_hi(w.x);
+    x[2] = bf16_lo(w.y);
+    x[3] = bf16_hi(w.y);
+}
+__device__ inline void widen(float4 w, float (&x)[4]) {
+    x[0] = w.x;
+    x[1] = w.y;
+    x[2] = w.z;
+    x[3] = w.w;
+}
+__device__ inline void narrow(const float (&x)[4], uint2 &w) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union { bf16x2 v; uint32_t u; } a, b;
+    a.v = bf16x2{(__bf16)x[0], (__bf16)x[1]};
+    b.v = bf16x2{(__bf16)x[2], (__bf16)x[3]};
+    w = make_uint2(a.u, b.u);
+}
+__device__ inline void narrow(const float (&x)[4], float4 &w) { w = make_float4(x[0], x[1], x[2], x[3]); }
+
+// The passes over a sequence's chunks, and the left operands of each: rows of K or Q
+// ([token x channel], read in the first half of a chunk) and columns ([channel x
+// token], read in the second), times the gates up to a token (before) or after it.
+//   forward: rows K before, Q before; columns K after; T and P
+//   save:    rows K before; columns K after; T and A (the states and the delta errors
+//            that the backward pass starts from)
+//   reverse: rows K after; columns K before, Q before; N^T and P^T (the gradient of the
+//            state, from the last chunk to the first)
+enum Pass { kForward, kSave, kReverse };
+
+// What a rule's operands carry.  All that a state or its gradient depends on keeps 22 bits:
+// K (and Q) in the hi part alone where the rows are bf16 and not folded with gates.  Q and P of the
+// forward pass reach the outputs only; for bf16 outputs (half a step: 2^-9) their hi
+// parts, and those of what they multiply, are enough (2^-12).
+template <int DK, bool KEYVEC, bool BF16, Pass PASS>
+struct PassShared {
+    static constexpr int NK = KEYVEC || !BF16 ? 2 : 1, KS = DK / 32, CT = DK / 16;
+    static constexpr int NQ = PASS == kForward ? (BF16 ? 1 : 2) : NK;  // parts of Q
+    static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (A, P^T)
+    static constexpr int TP = (2 + NP) * kPart;  // 16-byte pieces of the two triangular matrices
+    _Float16 K[NK][4][KS][kFrag];                // rows
+    _Float16 Q[PASS == kForward ? NQ : 1][PASS == kForward ? 4 : 1][PASS == kForward ? KS : 1][kFrag];
+    u32x4 tp[TP];
+    ChunkMeta m[2];                              // of even and of odd steps
+    _Float16 W[NK][CT][2][kFrag];                // columns
+    _Float16 V[PASS == kReverse ? NQ : 1][PASS == kReverse ? CT : 1][PASS == kReverse ? 2 : 1][kFrag];  // of Q
+};
+
+// The producing waves: 4 DK threads; a thread takes 4 tokens x 4 channels.
+template <int DK, bool KEYVEC, bool BF16, Pass PASS>
+struct Producer {
+    typedef PassShared<DK, KEYVEC, BF16, PASS> Shared;
+    typedef typename Raw4<BF16>::type raw;
+    static constexpr int NK = Shared::NK, NQ = Shared::NQ, TP = Shared::TP;
+    static constexpr int PT = 4 * DK, CG = DK / 4;           // threads; channel groups
+    static constexpr bool kQ = PASS != kSave;
+    raw k[4], q[kQ ? 4 : 1];
+    float4 a[KEYVEC ? 4 : 1], pre, suf, sk, sq;
+    u32x4 tp0, tp1, tp2, tp3, tp4, tp5, meta;
+    half4 w[NK][4], v[PASS == kReverse ? NQ : 1][4];  // columns of the chunk whose rows are written
+    int n;                           // tokens of the chunk in k, q and a
+    int tid, cg, tg;
+
+    __device__ inline void load(const ChunkArgs &A, int h, int first, int n_, size_t entry) {
+        n = n_;
+        const ChunkPrep *e = A.prep + entry;
+        const size_t base = ((size_t)first * A.s.H + h) * CG;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // past the last token its row again: T (N^T) has zeros in those columns and rows,
+            // so whatever finite values stand there add nothing
+            const uint32_t at = (uint32_t)min(4 * tg + i, n - 1) * (uint32_t)(A.s.H * CG) + cg;
+            k[i] = (static_cast<const raw *>(A.s.k) + base)[at];
+            if constexpr (kQ) q[i] = (static_cast<const raw *>(A.s.q) + base)[at];
+            if constexpr (KEYVEC) a[i] = (reinterpret_cast<const float4 *>(A.s.a) + base)[at];
+        }
+        if constexpr (KEYVEC) {
+            pre = *reinterpret_cast<const float4 *>(&A.gates[entry].pre[tg][4 * cg]);
+            suf = *reinterpret_cast<const float4 *>(&A.gates[entry].suf[tg][4 * cg]);
+        }
+        sk = *reinterpret_cast<const float4 *>(&e->m.sk[4 * tg]);
+        if constexpr (kQ) sq = *reinterpret_cast<const float4 *>(&e->m.sq[4 * tg]);
+        if (tid < kMeta) meta = reinterpret_cast<const u32x4 *>(&e->m)[tid];
+    }
+
+    // f(piece, its number) over this thread's pieces of the triangular matrices
+    template <class F>
+    __device__ inline void pieces(F f) {
+        f(tp0, tid);
+        f(tp1, tid + PT);
+        if (3 * PT <= TP || tid + 2 * PT < TP) f(tp2, tid + 2 * PT);
+        if constexpr (3 * PT < TP) f(tp3, tid + 3 * PT);
+        if constexpr (4 * PT < TP)
+            if (5 * PT <= TP || tid + 4 * PT < TP) f(tp4, tid + 4 * PT);
+        if constexpr (5 * PT < TP) f(tp5, tid + 5 * PT);
+    }
+
+    __device__ inline void load_tp(const ChunkArgs &A, size_t entry) {
+        const void *e = PASS == kReverse ? static_cast<const void *>(A.back + entry) : A.prep + entry;
+        pieces([&](u32x4 &x, int i) { x = reinterpret_cast<const u32x4 *>(e)[i]; });
+    }
+
+    // Gate of the thread's token i: 1 past the last token.
+    __device__ inline void gate(int i, float (&x)[4]) const {
+        widen(a[KEYVEC ? i : 0], x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = 4 * tg + i < n ? x[c] : 1.f;
+    }
+
+    // The chunk's rows into LDS, its columns into w and v.
+    __device__ inline void write_rows(Shared &sh, int which) {
+        float before[4], after[4][4];  // gate products up to and past a token
+        if constexpr (KEYVEC) {
+            widen(pre, before);
+            float s[4];
+            widen(suf, s);
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                float x[4];
+                gate(i, x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    after[i][c] = s[c];
+                    s[c] *= x[c];
+                }
+            }
+        }
+        const int g = cg & 3, ks = cg >> 3, eh = ((cg >> 2) & 1) * 4, rt = tg >> 2;
+        const float ek[4] = {sk.x, sk.y, sk.z, sk.w}, eq[4] = {sq.x, sq.y, sq.z, sq.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float kx[4], qx[4];
+            widen(k[i], kx);
+            if constexpr (kQ) widen(q[kQ ? i : 0], qx);
+            if constexpr (KEYVEC) {
+                float x[4];
+                gate(i, x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) before[c] *= x[c];
+            }
+            half4 kh, kl, qh, ql;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                _Float16 hi, lo;
+                if constexpr (NK == 2) {
+                    const float b = KEYVEC ? kx[c] * before[c] : kx[c], f = KEYVEC ? kx[c] * after[i][c] : kx[c];
+                    split(PASS == kReverse ? f : b, ek[i], hi, lo);
+                    kh[c] = hi;
+                    kl[c] = lo;
+                    if constexpr (KEYVEC) split(PASS == kReverse ? b : f, ek[i], hi, lo);
+                    w[0][c][i] = hi;
+                    w[NK - 1][c][i] = lo;
+                } else {
+                    kh[c] = w[0][c][i] = (_Float16)(kx[c] * ek[i]);
+                }
+                if constexpr (kQ) {
+                    split(KEYVEC ? qx[c] * before[c] : qx[c], eq[i], hi, lo);
+                    qh[c] = hi;
+                    ql[c] = lo;
+                    if constexpr (PASS == kReverse) {
+                        v[0][c][i] = hi;
+                        if constexpr (NQ == 2) v[NQ - 1][c][i] = lo;
+                    }
+                }
+            }
+            const int at = place_k(4 * (tg & 3) + i, g, ks) + eh;
+            *reinterpret_cast<half4 *>(&sh.K[0][rt][ks][at]) = kh;
+            if constexpr (NK == 2) *reinterpret_cast<half4 *>(&sh.K[NK - 1][rt][ks][at]) = kl;
+            if constexpr (PASS == kForward) {
+                *reinterpret_cast<half4 *>(&sh.Q[0][rt][ks][at]) = qh;
+                if constexpr (NQ == 2) *reinterpret_cast<half4 *>(&sh.Q[NQ - 1][rt][ks][at]) = ql;
+            }
+        }
+        if (tid < kMeta) reinterpret_cast<u32x4 *>(&sh.m[which])[tid] = meta;
+    }
+
+    __device__ inline void write_columns(Shared &sh) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int ch = 4 * cg + c, ct = ch >> 4;
+            const int at = place_w(ch & 15, tg & 3, ct) + ((tg >> 2) & 1) * 4;
+#pragma unroll
+            for (int l = 0; l < NK; ++l) *reinterpret_cast<half4 *>(&sh.W[l][ct][tg >> 3][at]) = w[l][c];
+            if constexpr (PASS == kReverse) {
+#pragma unroll
+                for (int l = 0; l < NQ; ++l) *reinterpret_cast<half4 *>(&sh.V[l][ct][tg >> 3][at]) = v[l][c];
+            }
+        }
+        pieces([&](u32x4 &x, int i) { sh.tp[i] = x; });
+    }
+
+    // All of a producing thread's work on a sequence of nc chunks: step i is chunk i, or nc - 1 - i
+    // in the reverse pass.
+    __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry) {
+        cg = tid % CG;
+        tg = tid / CG;
+        auto chunk = [&](int i) { return PASS == kReverse ? nc - 1 - i : i; };
+        auto fetch = [&](int i) {
+            const int c = chunk(i);
+            load(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry + (size_t)c * A.s.H);
+        };
+        fetch(0);
+        load_tp(A, entry + (size_t)chunk(0) * A.s.H);
+        write_rows(sh, 0);
+        if (nc > 1) fetch(1);
+        for (int i = 0; i < nc; ++i) {
+            lds_barrier();               // the rows of i stand; matrices and columns of i - 1 are done with
+            write_columns(sh);
+            if (i + 1 < nc) load_tp(A, entry + (size_t)chunk(i + 1) * A.s.H);
+            lds_barrier();               // matrices and columns of i stand; the rows of i are done with
+            if (i + 1 < nc) write_rows(sh, (i + 1) & 1);
+            if (i + 2 < nc) fetch(i + 2);
+        }
+    }
+};
+
+// Places in LDS whose constant offsets go into the reading instructions.  They are
+// formed anew where they are used: the compiler would otherwise keep the sums of place
+// and offset, dozens of registers, over the whole loop.
+typedef __attribute__((address_space(3))) const _Float16 *lds_half;
+typedef __attribute__((address_space(3))) const float *lds_float;
+
+__device__ inline lds_half half_at(const void *p, int at) {
+    lds_half q = (lds_half)p + at;
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline lds_float float_at(const void *p, int at) {
+    lds_float q = (lds_float)p + at;
+    asm volatile("" : "+v"(q));
+    return q;
+}
+__device__ inline half8 frag(lds_half p) { return *(__attribute__((address_space(3))) const half8 *)p; }
+
+// Two result tiles (rows 16 m.. and 16 m + 16..) times s as a right operand.
+__device__ inline void right(const floatx4 &x, const floatx4 &y, float s, half8 &hi, half8 &lo) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        _Float16 a, b;
+        split(x[e], s, a, b);
+        hi[e] = a;
+        lo[e] = b;
+        split(y[e], s, a, b);
+        hi[4 + e] = a;
+        lo[4 + e] = b;
+    }
+}
+
+template <int n>
+__device__ inline float column_max(const floatx4 (&x)[n]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(x[i][r]));
+    return max_groups(m);
+}
+
+__device__ inline floatx4 row_factors(lds_float p) {
+    return *(__attribute__((address_space(3))) const floatx4 *)p;
+}
+// Of the factors at `member` of ChunkMeta, those of row tile rt.
+constexpr int factors(size_t member, int rt) { return (int)(member / sizeof(float)) + 16 * rt; }
+
+// Four left fragments p + at(i), then their products: while a block of four multiplies, the
+// next one is on its way from LDS.
+__device__ inline void load4(half8 (&f)[4], lds_half p, int step, int first = 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i >= first) f[i] = frag(p + i * step);
+}
+__device__ inline void mul4(const half8 (&f)[4], half8 x, floatx4 (&Y)[4], int first = 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i >= first) Y[i] = mfma16(f[i], x, Y[i]);
+}
+
+// A lower triangular left operand (fragments at t, lo parts kTri further) times
+// a column block; `undo` takes the block's scale away.  FULL: with the lo parts.
+// f: the first block, on its way; `next` loads what comes after.
+template <bool FULL, class F>
+__device__ inline void lower(lds_half t, const floatx4 (&X)[4], floatx4 (&Y)[4], float &undo, half8 (&f)[4],
+                             half8 (&f2)[4], F next) {
+    const float s = scale_to(column_max(X), 13, undo);
+    half8 hi, lo, hi1, lo1;
+    right(X[0], X[1], s, hi, lo);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    // fragments of k step 0: rows 0, 1 at 0, 1, rows 2, 3 at 2, 4; of k step 1: rows 2, 3 at 3, 5
+    auto load = [&](half8 (&x)[4], int from) {
+        x[0] = frag(t + from * kFrag);
+        x[1] = frag(t + (from + 1) * kFrag);
+        x[2] = frag(t + (from + 2) * kFrag);
+        x[3] = frag(t + (from + 4) * kFrag);
+    };
+    auto load1 = [&](half8 (&x)[4], int from) {
+        x[2] = frag(t + (from + 3) * kFrag);
+        x[3] = frag(t + (from + 5) * kFrag);
+    };
+    if constexpr (FULL) {
+        load(f2, kTri);
+        mul4(f, hi, Y);
+        mul4(f, lo, Y);
+        __builtin_amdgcn_sched_barrier(0);
+        right(X[2], X[3], s, hi1, lo1);
+        load1(f, 0);
+        mul4(f2, hi, Y);
+        __builtin_amdgcn_sched_barrier(0);
+        load1(f2, kTri);
+        mul4(f, hi1, Y, 2);
+        mul4(f, lo1, Y, 2);
+        next();
+        mul4(f2, hi1, Y, 2);
+    } else {
+        right(X[2], X[3], s, hi1, lo1);
+        load1(f2, 0);
+        mul4(f, hi, Y);
+        next();
+        mul4(f2, hi1, Y, 2);
+    }
+}
+
+}  // namespace
+}  // namespace stq

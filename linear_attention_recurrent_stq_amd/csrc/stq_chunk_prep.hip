@@ -34,44 +34,6 @@ namespace {
 
 constexpr int LD = kC + 4;  // row stride of M in LDS
 
-// A choice whose both values are formed by every lane: a value read across lanes
-// inside a branch would find the other lanes switched off.
-__device__ inline float pick(bool c, float x, float y) { return c ? x : y; }
-
-// max over the lanes of a row of 16
-__device__ inline float max_row(float x) {
-    x = fmaxf(x, dpp<kRor + 8>(x));
-    x = fmaxf(x, dpp<kRor + 4>(x));
-    x = fmaxf(x, dpp<kRor + 2>(x));
-    return fmaxf(x, dpp<kRor + 1>(x));
-}
-__device__ inline float sum_groups(float x) {
-    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ inline floatx4 four(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
-
-// Eight consecutive channels as they are in memory.
-template <bool BF16> struct Row8;
-template <> struct Row8<true> {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 w;
-    __device__ void load(const void *p, size_t at) {
-        w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + at);
-    }
-    __device__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
-};
-template <> struct Row8<false> {
-    floatx4 x, y;
-    __device__ void load(const void *p, size_t at) {
-        x = four(static_cast<const float *>(p) + at);
-        y = four(static_cast<const float *>(p) + at + 4);
-    }
-    __device__ float get(int i) const { return i < 4 ? x[i] : y[i - 4]; }
-};
-
 template <int DK, bool BF16>
 struct Rows {
     Row8<BF16> k[DK / 32], q[DK / 32];
@@ -121,7 +83,47 @@ __device__ inline void store_tile(floatx4 x, floatx4 s, int I, int J, uint16_t (
     *reinterpret_cast<half4 *>(&to[1][f][at]) = lo;
 }
 
-// Row w of P's blocks.
+// The transpose of tile (I, J) times its rows' scale s (columns of the tile): a lane
+// holds four of its row's values as they stand in the fragment.
+__device__ inline void store_transposed(floatx4 x, float s, int I, int J, uint16_t (&to)[2][kTri][kFrag]) {
+    half4 hi, lo;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        _Float16 a, b;
+        split(x[r], s, a, b);
+        hi[r] = a;
+        lo[r] = b;
+    }
+    const int f = J < 2 ? 2 * J + (I >> 1) : 2 + J, at = (threadIdx.x & 63) * 8 + (I & 1) * 4;
+    *reinterpret_cast<half4 *>(&to[0][f][at]) = hi;
+    *reinterpret_cast<half4 *>(&to[1][f][at]) = lo;
+}
+
+// Row w of the blocks of P, transposed (backward); `tm`: [4][64] in LDS, written here.
+__device__ inline void store_pt(const floatx4 (&p)[4], float (*tm)[kC], ChunkMeta &m, ChunkBack &out) {
+    const int lane = threadIdx.x & 63, w = wave_index(), c16 = lane & 15;
+#pragma unroll
+    for (int J = 0; J < 4; ++J) {
+        float x = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x = fmaxf(x, J <= w ? fabsf(p[J][r]) : 0.f);
+        x = max_groups(x);
+        if (lane < 16) tm[w][16 * J + c16] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int J = 0; J < 4; ++J) {
+        float x = 0.f, inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = fmaxf(x, tm[i][16 * J + c16]);
+        const float sc = scale_to(x, 10, inv);
+        if (J <= (w | 1)) store_transposed(J <= w ? p[J] : floatx4{0.f, 0.f, 0.f, 0.f}, sc, w, J, out.P);
+        if (J == w && lane < 16) m.rpt[16 * J + c16] = inv;
+    }
+    __syncthreads();
+}
+
+// Row w of P's blocks (backward: of A's).
 __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
     const int lane = threadIdx.x & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
     floatx4 s, inv;
@@ -141,7 +143,9 @@ __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
 
 // From M = diag(beta) A in LDS (strictly lower; what lies above the diagonal is
 // not read) to T.
-__device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)[kC], const float *be, ChunkPrep &out) {
+template <bool BACK>
+__device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)[kC], const float *be, ChunkPrep &out,
+                               ChunkBack *back) {
     const int lane = threadIdx.x & 63, wave = wave_index(), j = lane & 15, g = lane >> 4;
     // inverse of the diagonal block `wave`, column j
     float x[16];
@@ -186,6 +190,21 @@ __device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)
         }
     }
     const float b = be[16 * wave + j];
+    if constexpr (BACK) {
+        float m = 0.f, inv;
+#pragma unroll
+        for (int I = 0; I < 4; ++I)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(t[I][r]));
+        const float s = scale_to(max_groups(m), 10, inv);
+#pragma unroll
+        for (int I = 0; I < 4; ++I)
+            if ((I | 1) >= wave) store_transposed(t[I], s, I, wave, back->N);
+        if (g == 0) {
+            out.m.rn[16 * wave + j] = inv;
+            out.m.be[16 * wave + j] = b;
+        }
+    }
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
         floatx4 m;
@@ -232,7 +251,8 @@ __device__ inline void order_sequences(const ChunkArgs &A, int *len) {
     }
 }
 
-template <int DK, bool BF16>
+// BACK: what the backward pass reads (A in P's place, N^T and P^T).
+template <int DK, bool BF16, bool BACK>
 __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     constexpr int KS = DK / 32;
     __shared__ union {
@@ -333,32 +353,24 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
         for (int r = 0; r < 4; ++r) {
             const int i = 4 * g + r;
             const float d = J < wave ? pi[r] * sj : i >= c16 ? dd[r] : 0.f;
-            big.M[16 * wave + i][16 * J + c16] = J < wave || i > c16 ? bi[r] * (aa[J][r] * d) : 0.f;
+            aa[J][r] = J < wave || i > c16 ? aa[J][r] * d : 0.f;
+            big.M[16 * wave + i][16 * J + c16] = bi[r] * aa[J][r];
             pp[J][r] = J < wave || i >= c16 ? pp[J][r] * d : 0.f;
         }
     }
-    store_p(pp, out);
-    __syncthreads();
-    store_t(big.M, X, tm, be, out);
-}
-
-// x s of eight channels as fp16 pairs
-__device__ inline void split8(const float (&x)[8], float s, half8 &hi, half8 &lo) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        _Float16 a, b;
-        split(x[e], s, a, b);
-        hi[e] = a;
-        lo[e] = b;
+    ChunkBack *back = nullptr;
+    if constexpr (BACK) {
+        back = A.back + (size_t)slot * s.H + h;
+        store_pt(pp, tm, out.m, *back);
+        store_p(aa, out);
+    } else {
+        store_p(pp, out);
     }
-}
-__device__ inline floatx4 mfma_pairs(half8 ah, half8 al, half8 bh, half8 bl, floatx4 c) {
-    c = mfma16(ah, bh, c);
-    c = mfma16(ah, bl, c);
-    return mfma16(al, bh, c);
+    __syncthreads();
+    store_t<BACK>(big.M, X, tm, be, out, back);
 }
 
-template <int DK, bool BF16>
+template <int DK, bool BF16, bool BACK>
 __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
     constexpr int KS = DK / 32;
     __shared__ union {
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
         float g[2][kC / 4][DK];      // products up to and after each four rows of a block, until M is written
     } big;
     __shared__ half8 Y[3][KS][2][64];  // k suf of waves 0 to 2
-    __shared__ __align__(16) float X[kC][20], tm[4][kC], dp[4][16][20], ik[kC], iq[kC], be[kC];
+    __shared__ __align__(16) float X[kC][20], tm[4][kC], dp[4][16][20], da_[4][16][20], ik[kC], iq[kC], be[kC];
     const SeqArgs &s = A.s;
     static_assert(sizeof(X) >= kOrdered * sizeof(int), "the lengths fit");
     if (blockIdx.x == (uint32_t)A.slots * (uint32_t)s.H) return order_sequences(A, reinterpret_cast<int *>(&X[0][0]));
@@ -404,33 +416,33 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
             const float a = on ? e < 4 ? a0[e & 3] : a1[e & 3] : 1.f, k = x.k[i].get(e), q = x.q[i].get(e);
             // 4x4 blocks
             dq[0] = __builtin_fmaf(q, k, dq[0]);
-            float v = dpp<kShr + 1>(k) * a;
+            float v = dpp0<kShr + 1>(k) * a;
             da[0] = __builtin_fmaf(k, v, da[0]);
             dq[1] = __builtin_fmaf(q, v, dq[1]);
-            float d = a * dpp<kShr + 1>(a);
-            v = dpp<kShr + 2>(k) * d;
+            float d = a * dpp0<kShr + 1>(a);
+            v = dpp0<kShr + 2>(k) * d;
             da[1] = __builtin_fmaf(k, v, da[1]);
             dq[2] = __builtin_fmaf(q, v, dq[2]);
-            d *= dpp<kShr + 2>(a);
-            v = dpp<kShr + 3>(k) * d;
+            d *= dpp0<kShr + 2>(a);
+            v = dpp0<kShr + 3>(k) * d;
             da[2] = __builtin_fmaf(k, v, da[2]);
             dq[3] = __builtin_fmaf(q, v, dq[3]);
             // products within 2, 4, 8 and 16 rows: up to the row (p), after it (f)
-            const float p2 = a * pick(b1, dpp<quad(0, 0, 2, 2)>(a), 1.f);
-            const float p4 = p2 * pick(b2, dpp<quad(1, 1, 1, 1)>(p2), 1.f);
-            const float t4 = dpp<quad(3, 3, 3, 3)>(p4);
-            const float p8 = p4 * pick(b4, dpp<kShr + 4>(t4), 1.f);
-            const float p16 = p8 * pick(b8, dpp<kBcast + 7>(p8), 1.f);
-            float f = pick(b1, 1.f, dpp<quad(1, 1, 3, 3)>(a));
-            f *= pick(b2, 1.f, dpp<quad(3, 3, 3, 3)>(p2));
+            const float p2 = a * pick(b1, dpp0<quad(0, 0, 2, 2)>(a), 1.f);
+            const float p4 = p2 * pick(b2, dpp0<quad(1, 1, 1, 1)>(p2), 1.f);
+            const float t4 = dpp0<quad(3, 3, 3, 3)>(p4);
+            const float p8 = p4 * pick(b4, dpp0<kShr + 4>(t4), 1.f);
+            const float p16 = p8 * pick(b8, dpp0<kBcast + 7>(p8), 1.f);
+            float f = pick(b1, 1.f, dpp0<quad(1, 1, 3, 3)>(a));
+            f *= pick(b2, 1.f, dpp0<quad(3, 3, 3, 3)>(p2));
             y4[e] = k * f;
-            f *= pick(b4, 1.f, dpp<kShl + 4>(t4));
+            f *= pick(b4, 1.f, dpp0<kShl + 4>(t4));
             y8[e] = k * f;
-            f *= pick(b8, 1.f, dpp<kBcast + 15>(p8));
+            f *= pick(b8, 1.f, dpp0<kBcast + 15>(p8));
             y16[e] = k * f;
             // the later half's rows of K, and of Q in the rows that the earlier half leaves free
-            z4[e] = pick(b4, k * p4 * x.sk, dpp<kShl + 4>(q * p4 * x.sq));
-            z8[e] = pick(b8, k * p8 * x.sk, dpp<kShl + 8>(q * p8 * x.sq));
+            z4[e] = pick(b4, k * p4 * x.sk, dpp0<kShl + 4>(q * p4 * x.sq));
+            z8[e] = pick(b8, k * p8 * x.sk, dpp0<kShl + 8>(q * p8 * x.sq));
             kp[i][e] = k * p16;
             qp[i][e] = q * p16;
             if ((c16 & 3) == 3) {
@@ -506,18 +518,18 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
         const float ikj = ik[16 * J + c16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            big.M[16 * w + 4 * g + r][16 * J + c16] = bi[r] * (aa[J][r] * iki[r] * ikj);
+            aa[J][r] = aa[J][r] * iki[r] * ikj;
+            big.M[16 * w + 4 * g + r][16 * J + c16] = bi[r] * aa[J][r];
             pp[J][r] = pp[J][r] * iqi[r] * ikj;
         }
     }
     // the diagonal block, from its cuts
-    float(*Md)[LD] = reinterpret_cast<float(*)[LD]>(&big.M[16 * w][16 * w]);
     const bool both = g & 1;         // cut 4: groups 1 and 3 hold A of rows 4 g .., 0 and 2 P of rows 4 g + 4 ..
     if (g < 2 ? c16 < 4 : c16 >= 8 && c16 < 12) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 4 * (g | 1) + r;
-            if (both) Md[i][c16] = be[16 * w + i] * (cut4[r] * ik[16 * w + i] * x.ik);
+            if (both) da_[w][i][c16] = cut4[r] * ik[16 * w + i] * x.ik;
             else dp[w][i][c16] = cut4[r] * iq[16 * w + i] * x.ik;
         }
     }
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 4 * (g | 2) + r;
-            if (g & 2) Md[i][c16] = be[16 * w + i] * (cut8[r] * ik[16 * w + i] * x.ik);
+            if (g & 2) da_[w][i][c16] = cut8[r] * ik[16 * w + i] * x.ik;
             else dp[w][i][c16] = cut8[r] * iq[16 * w + i] * x.ik;
         }
     }
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
         const float p = sum_groups(dq[d]), m = sum_groups(d ? da[d - 1] : 0.f);
         if (g == 0 && (c16 & 3) >= d) {
             dp[w][c16][c16 - d] = p;
-            Md[c16][c16 - d] = d ? be[row] * m : 0.f;
+            da_[w][c16][c16 - d] = m;
         }
     }
     __syncthreads();
@@ -542,26 +554,40 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
     for (int J = 0; J < 4; ++J)
         if (J == w)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) pp[J][r] = 4 * g + r >= c16 ? dp[w][4 * g + r][c16] : 0.f;
-    store_p(pp, out);
-    store_t(big.M, X, tm, be, out);
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * g + r;
+                pp[J][r] = i >= c16 ? dp[w][i][c16] : 0.f;
+                aa[J][r] = i > c16 ? da_[w][i][c16] : 0.f;
+                big.M[16 * w + i][16 * w + c16] = bi[r] * aa[J][r];
+            }
+    ChunkBack *back = nullptr;
+    if constexpr (BACK) {
+        back = A.back + (size_t)slot * s.H + h;
+        store_pt(pp, tm, out.m, *back);
+        store_p(aa, out);
+    } else {
+        store_p(pp, out);
+    }
+    __syncthreads();
+    store_t<BACK>(big.M, X, tm, be, out, back);
+}
+
+template <int DK, bool BACK>
+void go(const ChunkArgs &a, bool keyvec, bool bf16, hipStream_t s) {
+    const dim3 grid((unsigned)a.slots * (unsigned)a.s.H + (a.order ? 1u : 0u));
+    if (keyvec && bf16) k_prep_keyvec<DK, true, BACK><<<grid, 256, 0, s>>>(a);
+    else if (keyvec) k_prep_keyvec<DK, false, BACK><<<grid, 256, 0, s>>>(a);
+    else if (bf16) k_prep_scalar<DK, true, BACK><<<grid, 256, 0, s>>>(a);
+    else k_prep_scalar<DK, false, BACK><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_chunk_prep(const ChunkArgs &a, int dk, bool keyvec, bool bf16, hipStream_t s) {
-    const dim3 grid((unsigned)a.slots * (unsigned)a.s.H + (a.order ? 1u : 0u));
-    if (keyvec) {
-        if (dk == 64 && bf16) k_prep_keyvec<64, true><<<grid, 256, 0, s>>>(a);
-        else if (dk == 64) k_prep_keyvec<64, false><<<grid, 256, 0, s>>>(a);
-        else if (bf16) k_prep_keyvec<128, true><<<grid, 256, 0, s>>>(a);
-        else k_prep_keyvec<128, false><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (dk == 64 && bf16) k_prep_scalar<64, true><<<grid, 256, 0, s>>>(a);
-        else if (dk == 64) k_prep_scalar<64, false><<<grid, 256, 0, s>>>(a);
-        else if (bf16) k_prep_scalar<128, true><<<grid, 256, 0, s>>>(a);
-        else k_prep_scalar<128, false><<<grid, 256, 0, s>>>(a);
-    }
+    if (dk == 64 && a.back) go<64, true>(a, keyvec, bf16, s);
+    else if (dk == 64) go<64, false>(a, keyvec, bf16, s);
+    else if (a.back) go<128, true>(a, keyvec, bf16, s);
+    else go<128, false>(a, keyvec, bf16, s);
     return hipGetLastError();
 }
 

@@ -1,0 +1,283 @@
+// The pass of the state's gradient through the chunks of a sequence, from the last to the
+// first (the middle part of stq_chunk_backward).
+//
+// Per chunk, with dS the gradient of the state behind it and E_i = G_64/G_i:
+//   du = (K E) dS + P^T dO;   y = N^T du;   dV = beta y;
+//   dS = diag(G_64) dS + (Q G)^T dO - (K G)^T (beta y).
+// The gradient behind each chunk and y are kept for the chunk's own gradients.
+//
+// Laid out as the pass of the state (stq_chunk_fwd.hip): a wave owns 16 columns of dS in its
+// registers, the left operands come from LDS, where the producing waves replace one
+// half's while the other half multiplies.
+#include <type_traits>
+
+#include "stq_chunk_pass.h"
+
+namespace stq {
+namespace {
+
+// An upper triangular left operand (fragments at t in the order rows 0 (k steps 0, 1), 1 (0, 1),
+// 2 (1), 3 (1); lo parts kTri further) times a column block; `undo` takes the block's scale
+// away.  RLO: the block has a lo part (a block of bf16 values has none).
+template <bool RLO>
+__device__ inline void upper(lds_half t, const floatx4 (&X)[4], floatx4 (&Y)[4], float &undo) {
+    const float s = scale_to(column_max(X), 13, undo);
+    half8 hi, lo, f[4], f2[4];
+    auto load = [&](half8 (&x)[4], int from) {       // of k step 1
+        x[0] = frag(t + (from + 1) * kFrag);
+        x[1] = frag(t + (from + 3) * kFrag);
+        x[2] = frag(t + (from + 4) * kFrag);
+        x[3] = frag(t + (from + 5) * kFrag);
+    };
+    auto mul2 = [&](half8 (&x)[4], half8 b) {        // of k step 0: rows 0 and 1
+        Y[0] = mfma16(x[0], b, Y[0]);
+        Y[1] = mfma16(x[1], b, Y[1]);
+    };
+    load(f, 0);
+    right(X[2], X[3], s, hi, lo);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) Y[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    __builtin_amdgcn_sched_barrier(0);
+    load(f2, kTri);
+    mul4(f, hi, Y);
+    if constexpr (RLO) mul4(f, lo, Y);
+    __builtin_amdgcn_sched_barrier(0);
+    f[0] = frag(t);
+    f[1] = frag(t + 2 * kFrag);
+    mul4(f2, hi, Y);
+    right(X[0], X[1], s, hi, lo);
+    __builtin_amdgcn_sched_barrier(0);
+    f2[0] = frag(t + kTri * kFrag);
+    f2[1] = frag(t + (kTri + 2) * kFrag);
+    mul2(f, hi);
+    if constexpr (RLO) mul2(f, lo);
+    mul2(f2, hi);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int DK, int DV, bool KEYVEC, bool BF16>
+__global__ void __launch_bounds__(256 + 4 * DK) k_chunk_rev(const ChunkArgs A) {
+    typedef PassShared<DK, KEYVEC, BF16, kReverse> Shared;
+    typedef typename Raw4<BF16>::type raw;
+    constexpr int KS = Shared::KS, CT = Shared::CT, NK = Shared::NK, NQ = Shared::NQ;
+    constexpr int parts = DV / 64;       // workgroups of a (sequence, head)
+    __shared__ Shared sh;
+    const int H = A.s.H;
+    uint32_t seq, at_seq;
+    xcd_place(blockIdx.x, H * parts, seq, at_seq);
+    const int b = A.order ? A.order[seq] : seq, h = at_seq / parts, part = at_seq % parts;
+    int t0, t1;
+    seq_range(A.s, b, t0, t1);
+    const int nc = (t1 - t0 + kC - 1) / kC;
+    const size_t entry0 = (size_t)(t0 / kC + b) * H + h;
+
+    if (threadIdx.x >= 256) {
+        if (nc == 0) return;
+        Producer<DK, KEYVEC, BF16, kReverse> p;
+        p.tid = threadIdx.x - 256;
+        p.run(A, sh, h, t0, t1, nc, entry0);
+        return;
+    }
+
+    const int lane = threadIdx.x & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
+    const int col0 = (part * 4 + wave) * 16;
+    floatx4 S[CT];
+    const size_t state0 = ((size_t)b * H + h) * DK * DV + col0;
+    uint32_t at0 = 4 * g * DV + c16;     // of the lane's first value in the state
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[ct][r] = A.dlast ? (A.dlast + state0 + (16 * ct + r) * DV)[at0] : 0.f;
+    asm volatile("" : "+v"(at0));
+
+    // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
+    const int row0 = 4 * g + (c16 & 3);
+    const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
+    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
+    raw v[4];                            // dO of the next chunk
+    auto load_v = [&](int c) {
+        const raw *base = static_cast<const raw *>(A.dout) + (size_t)(t0 + c * kC) * row_step + col4;
+        const int n = t1 - t0 - c * kC;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + row0, n - 1) * row_step];
+    };
+    if (nc) load_v(nc - 1);
+
+    for (int i = 0; i < nc; ++i) {
+        const int c = nc - 1 - i, n = t1 - t0 - c * kC;
+        const size_t entry = entry0 + (size_t)c * H;
+        {
+            float *to = A.dS + entry * (DK * DV) + col0;
+            uint32_t at = 4 * g * DV + c16;
+            asm volatile("" : "+v"(at));
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) (to + (16 * ct + r) * DV)[at] = S[ct][r];
+        }
+        floatx4 R[4], D[4], y[4];
+        float undo;
+        const float s = scale_to(column_max(S), 13, undo);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) R[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+        half8 hi, lo, f[4], f2[4];
+        right(S[0], S[1], s, hi, lo);
+        lds_barrier();
+        const lds_float m = float_at(&sh.m[i & 1], 4 * g);
+        auto place = [&](int ks) { return half_at(&sh.K, place_k(c16, g, ks)) + ks * kFrag; };
+        lds_half kq = place(0);
+        constexpr int row = KS * kFrag;  // step to the next row tile
+        load4(f, kq, row);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const lds_half now = kq;
+            half8(&x0)[4] = NK == 1 && (ks & 1) ? f2 : f;
+            half8(&x1)[4] = NK == 1 && (ks & 1) ? f : f2;
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (NK == 2) load4(x1, now + 4 * row, row);
+            if (ks + 1 < KS) kq = place(ks + 1);
+            if constexpr (NK == 1)
+                if (ks + 1 < KS) load4(x1, kq, row);
+            mul4(x0, hi, R);
+            mul4(x0, lo, R);
+            if constexpr (NK == 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (ks + 1 < KS) load4(x0, kq, row);
+                mul4(x1, hi, R);
+            }
+            if (ks + 1 < KS) right(S[2 * ks + 2], S[2 * ks + 3], s, hi, lo);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const floatx4 rw = row_factors(m + factors(offsetof(ChunkMeta, rw), rt));
+            float x[4];
+            widen(v[rt], x);
+            const bool on = 16 * rt + row0 < n;  // past the last token: 0
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = on ? x[r] : 0.f;
+            quad_transpose(x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                D[rt][r] = x[r];
+                R[rt][r] = (R[rt][r] * rw[r]) * undo;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (c > 0) load_v(c - 1);
+        lds_barrier();
+        const lds_half t = half_at(&sh.tp, lane * 8);
+        upper<!BF16>(t + 2 * kTri * kFrag, D, y, undo);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const floatx4 x = row_factors(m + factors(offsetof(ChunkMeta, rpt), rt));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) R[rt][r] = __builtin_fmaf(y[rt][r] * x[r], undo, R[rt][r]);
+        }
+        upper<true>(t, R, y, undo);
+        float4 *ys = reinterpret_cast<float4 *>(A.y) + entry * (kC * DV / 4) + col0 / 4 + (c16 >> 2);
+        raw *dv = static_cast<raw *>(A.dv) + (size_t)(t0 + c * kC) * row_step + col4;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const floatx4 rn = row_factors(m + factors(offsetof(ChunkMeta, rn), rt)),
+                          be = row_factors(m + factors(offsetof(ChunkMeta, be), rt)),
+                          rk = row_factors(m + factors(offsetof(ChunkMeta, rk), rt)),
+                          rq = row_factors(m + factors(offsetof(ChunkMeta, rq), rt));
+            float x[4], z[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = (y[rt][r] * rn[r]) * undo;
+                z[r] = be[r] * x[r];
+                R[rt][r] = -z[r] * rk[r];
+                D[rt][r] *= rq[r];
+            }
+            quad_transpose(x);
+            quad_transpose(z);
+            ys[(16 * rt + row0) * (DV / 4)] = make_float4(x[0], x[1], x[2], x[3]);
+            raw out;
+            narrow(z, out);
+            if (16 * rt + row0 < n) dv[(uint32_t)(16 * rt + row0) * row_step] = out;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // both column blocks under one scale, for sums in the same registers
+        const float su = scale_to(fmaxf(column_max(R), column_max(D)), 13, undo);
+        half8 kh[2], kl[2], qh[2], ql[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            right(R[2 * ks], R[2 * ks + 1], su, kh[ks], kl[ks]);
+            right(D[2 * ks], D[2 * ks + 1], su, qh[ks], ql[ks]);
+        }
+        lds_half wb[4], vb[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            wb[j] = half_at(&sh.W, place_w(c16, g, j));
+            vb[j] = half_at(&sh.V, place_w(c16, g, j));
+        }
+        auto load_c = [&](half8 (&x)[4], const lds_half (&from)[4], int l, int c0, int ks) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = frag(from[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
+        };
+        load_c(f, wb, 0, 0, 0);
+#pragma unroll
+        for (int c0 = 0; c0 < CT; c0 += 4) {
+            floatx4 z[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bool more = ks == 0 || c0 + 4 < CT;
+                const int nc0 = ks ? c0 + 4 : c0, nks = ks ? 0 : 1;
+                __builtin_amdgcn_sched_barrier(0);
+                load_c(f2, vb, 0, c0, ks);
+                mul4(f, kh[ks], z);
+                mul4(f, kl[ks], z);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (NK == 2) load_c(f, wb, 1, c0, ks);
+                else if (more) load_c(f, wb, 0, nc0, nks);
+                mul4(f2, qh[ks], z);
+                mul4(f2, ql[ks], z);
+                if constexpr (NK == 2) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    load_c(f2, vb, NQ - 1, c0, ks);
+                    mul4(f, kh[ks], z);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (more) load_c(f, wb, 0, nc0, nks);
+                    mul4(f2, qh[ks], z);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const floatx4 d = row_factors(m + factors(offsetof(ChunkMeta, dec), c0 + j));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[c0 + j][r] = __builtin_fmaf(z[j][r], undo, S[c0 + j][r] * d[r]);
+            }
+        }
+    }
+    if (!A.dinitial) return;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) (A.dinitial + state0 + (16 * ct + r) * DV)[at0] = S[ct][r];
+}
+
+template <int DK, int DV>
+void go(const ChunkArgs &a, bool keyvec, bool bf16, hipStream_t s) {
+    const dim3 grid((unsigned)(DV / 64) * (unsigned)a.s.H * (unsigned)a.s.B);
+    constexpr int block = 256 + 4 * DK;
+    if (keyvec && bf16) k_chunk_rev<DK, DV, true, true><<<grid, block, 0, s>>>(a);
+    else if (keyvec) k_chunk_rev<DK, DV, true, false><<<grid, block, 0, s>>>(a);
+    else if (bf16) k_chunk_rev<DK, DV, false, true><<<grid, block, 0, s>>>(a);
+    else k_chunk_rev<DK, DV, false, false><<<grid, block, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_chunk_reverse(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s) {
+    if (dk == 64 && dv == 64) go<64, 64>(a, keyvec, bf16, s);
+    else if (dk == 64) go<64, 128>(a, keyvec, bf16, s);
+    else if (dv == 64) go<128, 64>(a, keyvec, bf16, s);
+    else go<128, 128>(a, keyvec, bf16, s);
+    return hipGetLastError();
+}
+
+}  // namespace stq

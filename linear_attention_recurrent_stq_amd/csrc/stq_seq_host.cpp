@@ -74,6 +74,32 @@ stq::SeqArgs seq_args(const stq_rule *r, int32_t B, int32_t N, const int32_t *cu
     return s;
 }
 
+// The parts of a chunk workspace at `base`, into *a (both may be NULL); its size.
+size_t carve(const stq_rule *r, int32_t B, int32_t N, bool backward, void *base, stq::ChunkArgs *a) {
+    const size_t entries = (size_t)stq::chunk_slots(N, B) * r->H;
+    size_t at = 0;
+    auto take = [&](size_t each) {
+        char *p = static_cast<char *>(base) + at;
+        at += (each * entries + 255) / 256 * 256;
+        return p;
+    };
+    stq::ChunkArgs none{};
+    if (!a) a = &none;
+    a->slots = stq::chunk_slots(N, B);
+    at = sizeof(int32_t) * stq::kOrdered;
+    a->order = B > 1 && B <= stq::kOrdered ? static_cast<int32_t *>(base) : nullptr;
+    a->prep = reinterpret_cast<stq::ChunkPrep *>(take(sizeof(stq::ChunkPrep)));
+    if (r->gate == STQ_GATE_KEYVEC) a->gates = reinterpret_cast<stq::ChunkGates *>(take(sizeof(stq::ChunkGates)));
+    if (backward) {
+        a->back = reinterpret_cast<stq::ChunkBack *>(take(sizeof(stq::ChunkBack)));
+        a->S = reinterpret_cast<float *>(take(sizeof(float) * r->d_k * r->d_v));
+        a->dS = reinterpret_cast<float *>(take(sizeof(float) * r->d_k * r->d_v));
+        a->w = reinterpret_cast<float *>(take(sizeof(float) * stq::kC * r->d_v));
+        a->y = reinterpret_cast<float *>(take(sizeof(float) * stq::kC * r->d_v));
+    }
+    return at;
+}
+
 }  // namespace
 
 extern "C" {
@@ -123,12 +149,9 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
     if (stq_status s = check_rule(rule)) return s;
     if (stq_status s = check_sizes(rule, B, N)) return s;
     if (!bytes) return fail(STQ_ERR_INVALID, "bytes is NULL");
-    if (backward) return fail(STQ_ERR_UNSUPPORTED, "no backward pass");
-    size_t each = sizeof(stq::ChunkPrep);
-    if (rule->gate == STQ_GATE_KEYVEC) each += sizeof(stq::ChunkGates);
-    if (((int64_t)N / stq::kC + B) * rule->H > INT32_MAX)
+    if (((int64_t)N / stq::kC + B) * rule->H >= INT32_MAX)
         return fail(STQ_ERR_UNSUPPORTED, "too many chunks for one call");
-    *bytes = each * (size_t)stq::chunk_slots(N, B) * rule->H + sizeof(int32_t) * stq::kOrdered;
+    *bytes = carve(rule, B, N, backward != 0, nullptr, nullptr);
     return STQ_OK;
 }
 
@@ -151,15 +174,49 @@ stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const i
     a.initial = d_initial;
     a.last = d_final;
     a.o = d_o;
-    a.slots = stq::chunk_slots(N, B);
-    if (B > 1 && B <= stq::kOrdered) a.order = static_cast<int32_t *>(d_workspace);
-    a.prep = reinterpret_cast<stq::ChunkPrep *>(static_cast<int32_t *>(d_workspace) + stq::kOrdered);
-    a.gates = reinterpret_cast<stq::ChunkGates *>(a.prep + (size_t)a.slots * rule->H);
+    carve(rule, B, N, false, d_workspace, &a);
     const bool keyvec = rule->gate == STQ_GATE_KEYVEC, bf16 = rule->io_dtype == STQ_BF16;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (stq_status s = launched(stq::launch_chunk_prep(a, rule->d_k, keyvec, bf16, st), "chunk preparation"))
         return s;
     return launched(stq::launch_chunk_forward(a, rule->d_k, rule->d_v, keyvec, bf16, st), "chunk forward");
+}
+
+stq_status stq_chunk_backward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
+                              const void *d_q, const void *d_k, const void *d_v, const float *d_a,
+                              const float *d_beta, const float *d_initial, const void *d_do,
+                              const float *d_dfinal, void *d_dq, void *d_dk, void *d_dv, float *d_da,
+                              float *d_dbeta, float *d_dinitial, void *d_workspace,
+                              size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    if (stq_status s = stq_chunk_workspace(rule, B, N, 1, &need)) return s;
+    if (B == 0) return STQ_OK;
+    if (stq_status s = check_ints(d_cu_seqlens, true, "cu_seqlens")) return s;
+    if (N > 0)  // without tokens the states' gradients are passed on and nothing else is touched
+        if (stq_status s = check_ptrs({d_q, d_k, d_v, d_a, d_beta, d_do, d_dq, d_dk, d_dv, d_da, d_dbeta})) return s;
+    if (stq_status s = check_ptrs({d_workspace})) return s;
+    if (!aligned(d_initial, 16) || !aligned(d_dfinal, 16) || !aligned(d_dinitial, 16))
+        return fail(STQ_ERR_ALIGN, "states must be 16-byte aligned");
+    if (workspace_bytes < need) return fail(STQ_ERR_TOO_SMALL, "workspace smaller than stq_chunk_workspace");
+    stq::ChunkArgs a{};
+    a.s = seq_args(rule, B, N, d_cu_seqlens, d_q, d_k, d_v, d_a, d_beta);
+    a.initial = d_initial;
+    a.dout = d_do;
+    a.dlast = d_dfinal;
+    a.dq = d_dq;
+    a.dk = d_dk;
+    a.dv = d_dv;
+    a.da = d_da;
+    a.dbeta = d_dbeta;
+    a.dinitial = d_dinitial;
+    carve(rule, B, N, true, d_workspace, &a);
+    const bool keyvec = rule->gate == STQ_GATE_KEYVEC, bf16 = rule->io_dtype == STQ_BF16;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int dk = rule->d_k, dv = rule->d_v;
+    if (stq_status s = launched(stq::launch_chunk_prep(a, dk, keyvec, bf16, st), "chunk preparation")) return s;
+    if (stq_status s = launched(stq::launch_chunk_forward(a, dk, dv, keyvec, bf16, st), "chunk states")) return s;
+    if (stq_status s = launched(stq::launch_chunk_reverse(a, dk, dv, keyvec, bf16, st), "chunk reverse")) return s;
+    return launched(stq::launch_chunk_grad(a, dk, dv, keyvec, bf16, st), "chunk gradients");
 }
 
 stq_status stq_verify_workspace(int32_t B, int32_t V, size_t *bytes) {

@@ -367,6 +367,160 @@ def test_chunk_python_refusals(stq):
     stq.chunk_forward(**good)
 
 
+# ----------------------------------------------------------------- backward
+# Each gradient is one more product, and one more pass through the chunks, away from the
+# inputs than an output: twice the products of the forward tolerance.  The
+# gradient of a gate is a difference of sums over a chunk's 64 tokens divided by it
+# (gates of 0.7 and more here): a factor sqrt(64) / 0.7, taken as 12.
+def _grad_tol(name, lens):
+    return 2 * _chunk_tol(lens) * (12 if name == "a" else 1)
+
+
+def _grads(stq, at, cu, x, keyvec, bf16, S0, do, dlast, plan=None, **kw):
+    H, dk, dv = x["q"].shape[1], x["q"].shape[2], x["v"].shape[2]
+    B = len(at) - 1
+    if plan is None:
+        plan = stq.ChunkPlan(H, dk, dv, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32,
+                             max_tokens=x["q"].shape[0], max_seqs=B, backward=True)
+        plan.workspace.fill_(255)
+    g = {m: torch.full_like(x[m], 7.0) for m in ("q", "k", "v", "a", "beta")}
+    g["state"] = torch.full((B, H, dk, dv), 7.0, device="cuda")
+    stq.chunk_backward(plan, cu, *[x[m] for m in ("q", "k", "v", "a", "beta")], do, g["q"], g["k"], g["v"], g["a"],
+                       g["beta"], initial_state=S0, d_final_state=dlast, d_initial_state=g["state"], **kw)
+    return g
+
+
+@pytest.mark.parametrize("lens", list(LENS))
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("keyvec,bf16", [(False, False), (False, True), (True, False), (True, True)])
+def test_chunk_backward(stq, lens, dk, dv, keyvec, bf16):
+    rng = np.random.default_rng(dk + 3 * dv)
+    lens, H = LENS[lens], 2
+    at, cu = _cu(lens)
+    n, B = at[-1] + 2, len(lens)
+    x, y = _inputs(rng, n, H, dk, dv, keyvec, bf16)
+    io = torch.bfloat16 if bf16 else torch.float32
+    do = torch.from_numpy(rng.normal(size=(n, H, dv)).astype(np.float32)).to(io)
+    S0, dlast = (rng.normal(size=(B, H, dk, dv)).astype(np.float32) for _ in range(2))
+    names = ("q", "k", "v", "a", "beta")
+    for first, last in ((S0, dlast), (None, None)):
+        g = _grads(stq, at, cu, x, keyvec, bf16, None if first is None else torch.from_numpy(first).cuda(), do.cuda(),
+                   None if last is None else torch.from_numpy(last).cuda())
+        zero = np.zeros_like(S0)
+        want = seqref.backward(at, *(y[m] for m in names), zero if first is None else first, do.double().numpy(),
+                               zero if last is None else last)
+        for m in names:
+            got = g[m].double().cpu().numpy()
+            assert (got[at[-1]:] == 7).all()
+            _within(got[:at[-1]], want[m][:at[-1]], _grad_tol(m, lens) + _io_step(bf16 and m in "qkv"))
+        _within(g["state"].cpu().numpy(), want["state"], _grad_tol("state", lens))
+
+
+@pytest.mark.parametrize("keyvec", [False, True])
+@pytest.mark.parametrize("what", ["strong", "beta0", "tiny", "same keys", "zero"])
+def test_chunk_backward_extremes(stq, keyvec, what):
+    rng = np.random.default_rng(21)
+    lens, H, d = [150, 64], 2, 128
+    at, cu = _cu(lens)
+    x, _ = _inputs(rng, at[-1], H, d, d, keyvec, False)
+    S0, dlast = (rng.normal(size=(2, H, d, d)).astype(np.float32) for _ in range(2))
+    do = rng.normal(size=(at[-1], H, d)).astype(np.float32)
+    if what == "strong":
+        x["a"].mul_(0.05)
+        x["a"][::3].mul_(0.05)
+    elif what == "beta0":
+        x["beta"][::2] = 0.0
+        x["beta"][1::4] = 1.0
+    elif what == "tiny":
+        for m in ("v", "q"):
+            x[m].mul_(2.0 ** -30)
+        S0 *= np.float32(2.0 ** -30)
+        do *= np.float32(2.0 ** -30)
+        dlast *= np.float32(2.0 ** -60)
+    elif what == "same keys":
+        x["k"][:] = x["k"][0]
+    elif what == "zero":
+        for m in ("q", "k", "v", "beta"):
+            x[m].zero_()
+    y = {m: t.double().cpu().numpy() for m, t in x.items()}
+    g = _grads(stq, at, cu, x, keyvec, False, torch.from_numpy(S0).cuda(), torch.from_numpy(do).cuda(),
+               torch.from_numpy(dlast).cuda())
+    want = seqref.backward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), S0, do, dlast)
+    for m in g:
+        got, w = g[m].cpu().numpy().astype(np.float64), want[m]
+        if m == "a":                     # what is formed in sums is a times it
+            got, w = got * y["a"], w * y["a"]
+        _within(got, w, _grad_tol(m, lens))
+
+
+@pytest.mark.parametrize("keyvec", [False, True])
+def test_chunk_backward_against_differences(stq, keyvec):
+    """Directional differences of the forward kernel's own loss: in fp32, so the
+    outputs' errors (relative _chunk_tol of a loss of size sqrt(outputs)) over twice
+    the step bound the comparison, beside the step's square."""
+    rng = np.random.default_rng(31)
+    lens, H, d = [70, 9], 2, 64
+    at, cu = _cu(lens)
+    x, _ = _inputs(rng, at[-1], H, d, d, keyvec, False)
+    S0, dlast = (torch.from_numpy(rng.normal(size=(2, H, d, d)).astype(np.float32)).cuda() for _ in range(2))
+    do = torch.from_numpy(rng.normal(size=(at[-1], H, d)).astype(np.float32)).cuda()
+    names = ("q", "k", "v", "a", "beta")
+    g = _grads(stq, at, cu, x, keyvec, False, S0, do, dlast)
+    plan = stq.ChunkPlan(H, d, d, gate=int(keyvec), io_dtype=stq.F32, max_tokens=at[-1], max_seqs=2)
+
+    def loss(z, S):
+        o, last = torch.empty_like(x["v"]), torch.empty_like(S)
+        stq.chunk_forward(plan, cu, *[z[m] for m in names], o, initial_state=S, final_state=last)
+        return float((o.double() * do).sum() + (last.double() * dlast).sum()), float(
+            (o.double() * do).norm() + (last.double() * dlast).norm())
+
+    eps = 1e-2
+    for m in names + ("state",):
+        base = S0 if m == "state" else x[m]
+        v = torch.from_numpy(rng.normal(size=tuple(base.shape)).astype(np.float32)).cuda()
+        v *= 0.2 / v.abs().max()
+        put = lambda s: (x, base + s * v) if m == "state" else (dict(x, **{m: base + s * v}), S0)
+        (hi, size), (lo, _) = loss(*put(eps)), loss(*put(-eps))
+        (hi2, _), (lo2, _) = loss(*put(eps / 2)), loss(*put(-eps / 2))
+        d1, d2 = (hi - lo) / (2 * eps), (hi2 - lo2) / eps
+        want = float((g[m].double() * v).sum())
+        # d2's own truncation is a third of its distance from d1
+        assert abs(d2 - want) < abs(d1 - d2) + 2 * _chunk_tol(lens) * size / eps
+
+
+def test_chunk_backward_alone_and_in_a_graph(stq):
+    """The same bits alone and in a batch, and at every replay of a captured call."""
+    rng = np.random.default_rng(41)
+    lens, H, d = [90, 64, 5], 2, 64
+    at, cu = _cu(lens)
+    x, _ = _inputs(rng, at[-1], H, d, d, True, True)
+    do = x["v"] * 0.5
+    S0, dl = (torch.from_numpy(rng.normal(size=(3, H, d, d)).astype(np.float32)).cuda() for _ in range(2))
+    full = _grads(stq, at, cu, x, True, True, S0, do, dl)
+    one = _grads(stq, at[:2], cu[:2], {m: x[m][:90].contiguous() for m in x}, True, True, S0[:1], do[:90].contiguous(),
+                 dl[:1])
+    for m in full:
+        assert torch.equal(one[m], full[m][:len(one[m])]), m
+    plan = stq.ChunkPlan(H, d, d, gate=1, max_tokens=at[-1], max_seqs=3, backward=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _grads(stq, at, cu, x, True, True, S0, do, dl, plan)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _grads(stq, at, cu, x, True, True, S0, do, dl, plan)
+    for i in range(3):
+        new, _ = _inputs(rng, at[-1], H, d, d, True, True)
+        for m in x:
+            x[m].copy_(new[m])
+        want = _grads(stq, at, cu, new, True, True, S0, do, dl)
+        graph.replay()
+        torch.cuda.synchronize()
+        for m in got:
+            assert torch.equal(got[m], want[m]), (i, m)
+
+
 # ------------------------------------------------------------------- verify
 
 def _probs(rng, shape, bf16, hot=2.0):
