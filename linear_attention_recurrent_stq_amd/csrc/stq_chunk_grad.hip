@@ -130,7 +130,6 @@ __device__ inline void distances(const Sh &sh, int w, int c16, const float (&k)[
     a1 = hi ? a1 : 0.f;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        __builtin_amdgcn_sched_barrier(0);   // (or every distance's moves are made ahead, and spill)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             // gates of i - D + 1 .. i, and of i + 1 .. i + D
@@ -141,6 +140,9 @@ __device__ inline void distances(const Sh &sh, int w, int c16, const float (&k)[
             dr[t][r] = __builtin_fmaf(a0, x, dr[t][r]);
             const float y = __builtin_fmaf(p1, dpp0<kShl + D>(q[t][r]), a1 * dpp0<kShl + D>(k[t][r]));
             dw[t][r] = __builtin_fmaf(after[t][r], y, dw[t][r]);
+            // formed here: moved to where the sums are used, which lanes past the last token skip, they
+            // would keep every distance's values of other lanes until then
+            asm volatile("" : "+v"(dq[t][r]), "+v"(dr[t][r]), "+v"(dw[t][r]));
         }
     }
     if constexpr (D < 15) distances<D + 1, T>(sh, w, c16, k, q, a, before, after, dq, dr, dw);
