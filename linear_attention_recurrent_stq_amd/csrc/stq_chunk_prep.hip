@@ -371,14 +371,23 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
 }
 
 template <int DK, bool BF16, bool BACK>
-__global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
+__global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
     constexpr int KS = DK / 32;
     __shared__ union {
         float M[kC][LD];
         float g[2][kC / 4][DK];      // products up to and after each four rows of a block, until M is written
     } big;
-    __shared__ half8 Y[3][KS][2][64];  // k suf of waves 0 to 2
-    __shared__ __align__(16) float X[kC][20], tm[4][kC], dp[4][16][20], da_[4][16][20], ik[kC], iq[kC], be[kC];
+    __shared__ __align__(16) union {
+        half8 Y[3][KS][2][64];       // k suf of waves 0 to 2
+        struct {
+            float X[kC][20], dp[4][16][20], da[4][16][20];  // once Y is done with
+        } f;
+    } two;
+    auto &Y = two.Y;
+    auto &X = two.f.X;
+    auto &dp = two.f.dp;
+    auto &da_ = two.f.da;
+    __shared__ __align__(16) float tm[4][kC], ik[kC], iq[kC], be[kC];
     const SeqArgs &s = A.s;
     static_assert(sizeof(X) >= kOrdered * sizeof(int), "the lengths fit");
     if (blockIdx.x == (uint32_t)A.slots * (uint32_t)s.H) return order_sequences(A, reinterpret_cast<int *>(&X[0][0]));
@@ -406,11 +415,17 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
     float kp[KS][8], qp[KS][8];      // k pre, q pre
     floatx4 cut4 = {0.f, 0.f, 0.f, 0.f}, cut8 = cut4;
     float da[3] = {}, dq[4] = {};    // 4x4 blocks: rows d earlier, A for d = 1, 2, 3 and P for d = 0 .. 3
+    floatx4 n0 = four(s.a + x.at), n1 = four(s.a + x.at + 4);  // the next channels' gates
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
+        const floatx4 a0 = n0, a1 = n1;
+        if (i + 1 < KS) {
+            n0 = four(s.a + x.at + 32 * i + 32);
+            n1 = four(s.a + x.at + 32 * i + 36);
+        }
         __builtin_amdgcn_sched_barrier(0);
-        const floatx4 a0 = four(s.a + x.at + 32 * i), a1 = four(s.a + x.at + 32 * i + 4);
         float z4[8], z8[8], y4[8], y8[8], y16[8];
+        floatx4 pe[2], fe[2];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float a = on ? e < 4 ? a0[e & 3] : a1[e & 3] : 1.f, k = x.k[i].get(e), q = x.q[i].get(e);
@@ -445,9 +460,17 @@ __global__ void __launch_bounds__(256) k_prep_keyvec(const ChunkArgs A) {
             z8[e] = pick(b8, k * p8 * x.sk, dpp0<kShl + 8>(q * p8 * x.sq));
             kp[i][e] = k * p16;
             qp[i][e] = q * p16;
-            if ((c16 & 3) == 3) {
-                big.g[0][row >> 2][32 * i + 8 * g + e] = p16;
-                big.g[1][row >> 2][32 * i + 8 * g + e] = f;
+            asm volatile("" : "+v"(kp[i][e]), "+v"(qp[i][e]));  // (formed here, not where a wave uses them)
+            pe[e >> 2][e & 3] = p16;
+            fe[e >> 2][e & 3] = f;
+        }
+        // (sums formed here: moved to where they are used they would keep every term)
+        asm volatile("" : "+v"(da[0]), "+v"(da[1]), "+v"(da[2]), "+v"(dq[0]), "+v"(dq[1]), "+v"(dq[2]), "+v"(dq[3]));
+        if ((c16 & 3) == 3) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                *reinterpret_cast<floatx4 *>(&big.g[0][row >> 2][32 * i + 8 * g + 4 * e]) = pe[e];
+                *reinterpret_cast<floatx4 *>(&big.g[1][row >> 2][32 * i + 8 * g + 4 * e]) = fe[e];
             }
         }
         half8 zh, zl, yh, yl;
