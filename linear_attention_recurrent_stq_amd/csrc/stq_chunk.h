@@ -41,8 +41,8 @@ struct ChunkMeta {
     float be[kC];                    // backward: beta, 0 past the last token
 };
 struct ChunkPrep {
-    uint16_t T[2][kTri][kFrag];
-    uint16_t P[2][kTri][kFrag];      // backward: A
+    uint16_t T[2][kTri][kFrag];      // backward: N' = (I + A diag(beta))^-1
+    uint16_t P[2][kTri][kFrag];
     ChunkMeta m;
 };
 // The backward pass's other matrices: N^T, N = (I + diag(beta) A)^-1, and P^T, upper
@@ -71,7 +71,8 @@ struct ChunkArgs {
     // The backward pass (back not nullptr): per (chunk, head)
     ChunkBack *back;
     float *S, *dS;                   // first state; gradient of the last one [d_k,d_v]
-    float *w, *y;                    // delta errors; gradients of u through N^T [64,d_v]
+    float *w, *y;                    // delta errors (u = beta w); gradients of u through N^T [64,d_v]
+                                     // (these four as result tiles: [column / 16][row / 16][lane][4])
     const void *dout;                // [N,H,d_v] io dtype
     const float *dlast;              // [B,H,d_k,d_v] or nullptr
     void *dq, *dk, *dv;              // io dtype

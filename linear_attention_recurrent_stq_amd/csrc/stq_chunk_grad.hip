@@ -15,7 +15,7 @@
 //
 // Everything is formed transposed, tokens in the lanes: wave (I, half) takes the 16 tokens
 // of block I and half of the channels.  Its own dO, y and w are right operands in its registers
-// (eight consecutive values of a row a lane); the states and the other tokens' rows are
+// (eight values of a row a lane); the states and the other tokens' rows are
 // left operands in LDS, in the same form.  dP and dA come out as tiles that are right operands of
 // the products with K^T and Q^T as they stand, both ways round (j up to I and j from I on), ten
 // 16x16 tiles in every wave.
@@ -84,6 +84,20 @@ struct GradShared {
     float te[4][DK], tf[4][DK];          // key-vector gates: sums of e and f of the blocks
     float es[2][kC], fs[2][kC];          // scalar gates: e and f by halves of the channels
 };
+
+// The passes leave states, w and y as result tiles, [tile][lane][4]: lane (c, g) has rows 4 g .. + 3
+// of column c.  Of a tile, lane (c, g) here gets columns 4 g .. + 3 of row c: quads read one row's
+// four groups, and turn them.
+__device__ inline int untwist() {
+    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+    return 4 * g + (c16 & 3) + 16 * (c16 >> 2);
+}
+__device__ inline void load_turned(const float *tile, float (&x)[4]) {
+    const floatx4 v = four(tile + 4 * untwist());
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = v[r];
+    quad_transpose(x);
+}
 
 // Left (lh, ll) times right (rh, rl) operand; lo parts as far as they are there.
 template <bool LL, bool RL>
@@ -172,17 +186,18 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
     float own_io, own_iy, own_iw;
     {
         float x[DVS][8], z[DVS][8], mx = 0.f, dot = 0.f, sc;
-        const float *yp = A.y + (entry * kC + own) * DV + 8 * g, *wp = A.w + (entry * kC + own) * DV + 8 * g;
+        const float *yp = A.y + entry * (kC * DV), *wp = A.w + entry * (kC * DV);
 #pragma unroll
-        for (int i = 0; i < DVS; ++i) {
-            const floatx4 a0 = four(yp + 32 * i), a1 = four(yp + 32 * i + 4), b0 = four(wp + 32 * i),
-                          b1 = four(wp + 32 * i + 4);
+        for (int cb = 0; cb < DV / 16; ++cb) {
+            float a[4], b[4];
+            load_turned(yp + (cb * 4 + w) * 256, a);
+            load_turned(wp + (cb * 4 + w) * 256, b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[i][e] = e < 4 ? a0[e & 3] : a1[e & 3];
-                z[i][e] = e < 4 ? b0[e & 3] : b1[e & 3];
-                dot = __builtin_fmaf(x[i][e], z[i][e], dot);
-                mx = fmaxf(mx, fabsf(x[i][e]));
+            for (int e = 0; e < 4; ++e) {
+                x[cb >> 1][4 * (cb & 1) + e] = a[e];
+                z[cb >> 1][4 * (cb & 1) + e] = b[e];
+                dot = __builtin_fmaf(a[e], b[e], dot);
+                mx = fmaxf(mx, fabsf(a[e]));
             }
         }
         sc = scale_to(max_groups(mx), 13, own_iy);
@@ -198,17 +213,17 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
         for (int i = 0; i < DVS; ++i) split8(z[i], sc, wh[i], wl[i]);
         dot = sum_groups(dot);
         if (half == 0 && g == 0 && on) A.dbeta[tok] = dot;
-        Row8<BF16> o[DVS];
         mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < DVS; ++i) o[i].load(A.dout, tok * DV + 32 * i + 8 * g);
+        for (int cb = 0; cb < DV / 16; ++cb) {
+            float a[4];
+            static_cast<const Four<BF16> *>(A.dout)[(tok * DV + 16 * cb) / 4 + g].get(a);
 #pragma unroll
-        for (int i = 0; i < DVS; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[i][e] = on ? o[i].get(e) : 0.f;  // past the last token: 0
-                mx = fmaxf(mx, fabsf(x[i][e]));
+            for (int e = 0; e < 4; ++e) {
+                x[cb >> 1][4 * (cb & 1) + e] = on ? a[e] : 0.f;  // past the last token: 0
+                mx = fmaxf(mx, fabsf(x[cb >> 1][4 * (cb & 1) + e]));
             }
+        }
         sc = scale_to(max_groups(mx), 13, own_io);
 #pragma unroll
         for (int i = 0; i < DVS; ++i) {
@@ -346,45 +361,41 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
 
     // ---- the states' parts: S dO, S y, dS w over the wave's half of the channels
     floatx4 vq[T], vk[T], vw[T];
-    constexpr int LR = DV / 8, ROWS = 512 / LR;  // lanes of a row; rows at a time
     auto stage = [&](const float *from, const float *dot_with) {
         __syncthreads();
+        const int ct = wave_index();
+        if (ct < CT) {                   // a wave turns 16 channels
+            float x[DV / 16][4], mx = 0.f, inv;
+            floatx4 dot = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int pass = 0; pass < DK / ROWS; ++pass) {
-            const int row = pass * ROWS + tid / LR, l = tid % LR;
-            const float *p = from + row * DV + 8 * l;
-            const floatx4 x0 = four(p), x1 = four(p + 4);
-            float x[8], mx = 0.f, dot = 0.f;
+            for (int cb = 0; cb < DV / 16; ++cb) {
+                const floatx4 v = four(from + (cb * CT + ct) * 256 + 4 * untwist());
+                if (dot_with) dot += v * four(dot_with + (cb * CT + ct) * 256 + 4 * untwist());
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = e < 4 ? x0[e & 3] : x1[e & 3];
-                mx = fmaxf(mx, fabsf(x[e]));
-            }
-            if (dot_with) {
-                const floatx4 z0 = four(dot_with + row * DV + 8 * l), z1 = four(dot_with + row * DV + 8 * l + 4);
+                for (int r = 0; r < 4; ++r) x[cb][r] = v[r];
+                quad_transpose(x[cb]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(x[e], e < 4 ? z0[e & 3] : z1[e & 3], dot);
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(x[cb][r]));
             }
-            // over the row's 8 or 16 lanes: the mirrored lane, then within quads
-            if constexpr (LR == 16) {
-                mx = fmaxf(mx, dpp0<0x140>(mx));
-                dot += dpp0<0x140>(dot);
+            const float sc = scale_to(max_groups(mx), 10, inv);
+#pragma unroll
+            for (int cb = 0; cb < DV / 16; ++cb) {
+                half4 hi, lo;
+                split4(floatx4{x[cb][0], x[cb][1], x[cb][2], x[cb][3]}, sc, hi, lo);
+                const int at = place(c16, g, cb >> 1);
+                reinterpret_cast<half4 *>(&sh.st[0][ct][cb >> 1][at])[cb & 1] = hi;
+                reinterpret_cast<half4 *>(&sh.st[1][ct][cb >> 1][at])[cb & 1] = lo;
             }
-            mx = fmaxf(mx, dpp0<0x141>(mx));
-            dot += dpp0<0x141>(dot);
-            mx = fmaxf(mx, dpp0<quad(1, 0, 3, 2)>(mx));
-            dot += dpp0<quad(1, 0, 3, 2)>(dot);
-            mx = fmaxf(mx, dpp0<quad(2, 3, 0, 1)>(mx));
-            dot += dpp0<quad(2, 3, 0, 1)>(dot);
-            float inv;
-            half8 hi, lo;
-            split8(x, scale_to(mx, 10, inv), hi, lo);
-            const int at = place(row & 15, l & 3, l >> 2);
-            sh.st[0][row >> 4][l >> 2][at] = hi;
-            sh.st[1][row >> 4][l >> 2][at] = lo;
-            if (l == 0) {
-                sh.srow[row] = inv;
-                if (dot_with) sh.rho[row] = dot;
+            if (g == 0) sh.srow[16 * ct + c16] = inv;
+            if (dot_with) {              // before the turn a lane has a column of channels 4 (c16 / 4) ..
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float d = dot[r];
+                    d += dpp0<quad(1, 0, 3, 2)>(d);
+                    d += dpp0<quad(2, 3, 0, 1)>(d);
+                    dot[r] = sum_groups(d);
+                }
+                if (g == 0 && (c16 & 3) == 0) *reinterpret_cast<floatx4 *>(&sh.rho[16 * ct + c16]) = dot;
             }
         }
         __syncthreads();

@@ -10,7 +10,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMeta = sizeof(ChunkMeta) / 16;  // 16-byte pieces
-constexpr int kPart = kTri * kFrag * 2 / 16;   // of T's or P's hi or lo part
+constexpr int kPart = kTri * kFrag * 2 / 16;   // of a triangular matrix's hi or lo part
 
 // Where lane (row, g)'s eight halves stand in a fragment: rows are permuted so
 // that the producers' writes (fixed row, all g and k steps) and the readers'
@@ -44,32 +44,59 @@ __device__ inline void narrow(const float (&x)[4], uint2 &w) {
 }
 __device__ inline void narrow(const float (&x)[4], float4 &w) { w = make_float4(x[0], x[1], x[2], x[3]); }
 
-// The passes over a sequence's chunks, and the left operands of each: rows of K or Q
-// ([token x channel], read in the first half of a chunk) and columns ([channel x
-// token], read in the second), times the gates up to a token (before) or after it.
-//   forward: rows K before, Q before; columns K after; T and P
-//   save:    rows K before; columns K after; T and A (the states and the delta errors
-//            that the backward pass starts from)
-//   reverse: rows K after; columns K before, Q before; N^T and P^T (the gradient of the
-//            state, from the last chunk to the first)
+// The passes over a sequence's chunks.  Every chunk (step i) has two halves, A and B, parted by
+// barriers; what one half reads is replaced while the other half runs:
+//   forward: A reads K, Q [token x channel] times the gates up to a token (before);
+//            B reads K^T [channel x token] times those after it, T, and P of the step before
+//   save:    A K before; B K^T after, N' (in T's place).  Leaves each chunk's first state and delta
+//            errors w, which the backward pass starts from
+//   reverse: A K after, Q^T before, P^T; B K^T before, N^T.  The state's gradient, last chunk first
 enum Pass { kForward, kSave, kReverse };
 
 // What a rule's operands carry.  All that a state or its gradient depends on keeps 22 bits:
-// K (and Q) in the hi part alone where the rows are bf16 and not folded with gates.  Q and P of the
-// forward pass reach the outputs only; for bf16 outputs (half a step: 2^-9) their hi
+// K (and Q^T) in the hi part alone where the rows are bf16 and not folded with gates.  Q and P of
+// the forward pass reach the outputs only; for bf16 outputs (half a step: 2^-9) their hi
 // parts, and those of what they multiply, are enough (2^-12).
+//
+// NW: columns of 16 of a workgroup, each with a wave that carries the state and (forward, reverse) one
+// that helps it: four, or two where the fragments of four do not fit in LDS.
 template <int DK, bool KEYVEC, bool BF16, Pass PASS>
 struct PassShared {
     static constexpr int NK = KEYVEC || !BF16 ? 2 : 1, KS = DK / 32, CT = DK / 16;
     static constexpr int NQ = PASS == kForward ? (BF16 ? 1 : 2) : NK;  // parts of Q
-    static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (A, P^T)
-    static constexpr int TP = (2 + NP) * kPart;  // 16-byte pieces of the two triangular matrices
-    _Float16 K[NK][4][KS][kFrag];                // rows
-    _Float16 Q[PASS == kForward ? NQ : 1][PASS == kForward ? 4 : 1][PASS == kForward ? KS : 1][kFrag];
-    u32x4 tp[TP];
-    ChunkMeta m[2];                              // of even and of odd steps
-    _Float16 W[NK][CT][2][kFrag];                // columns
-    _Float16 V[PASS == kReverse ? NQ : 1][PASS == kReverse ? CT : 1][PASS == kReverse ? 2 : 1][kFrag];  // of Q
+    static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (P^T)
+    static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse;
+    static constexpr int NW = DK == 128 && ((FWD && !BF16) || (REV && NK == 2)) ? 2 : 4;
+    static constexpr int NH = PASS == kSave ? 0 : NW;                  // helping waves
+    _Float16 K[NK][4][KS][kFrag];
+    _Float16 Q[FWD ? NQ : 1][FWD ? 4 : 1][FWD ? KS : 1][kFrag];
+    u32x4 T[2 * kPart];                          // T, N' or N^T
+    u32x4 P[PASS == kSave ? 1 : NP * kPart];     // P or P^T
+    ChunkMeta m[3];                              // of three steps in turn
+    _Float16 W[NK][CT][2][kFrag];                // K^T
+    _Float16 V[REV ? NQ : 1][REV ? CT : 1][REV ? 2 : 1][kFrag];  // Q^T
+    // forward, carrier to helper: the state and u as right operands, and what undoes their scales
+    _Float16 sf[FWD ? NQ : 1][FWD ? NW : 1][FWD ? KS : 1][kFrag], uf[FWD ? NQ : 1][FWD ? NW : 1][FWD ? 2 : 1][kFrag];
+    float us[NW][16], uu[NW][16];
+    // reverse, helper to carrier: P^T dO and (Q before)^T dO, as result tiles
+    floatx4 pd[REV ? NW : 1][4][REV ? 64 : 1], zd[REV ? NW : 1][REV ? CT : 1][REV ? 64 : 1];
+};
+
+// COUNT pieces of 16 bytes, PT threads.
+template <int COUNT, int PT>
+struct Pieces {
+    static constexpr int n = (COUNT + PT - 1) / PT;
+    u32x4 x[n];
+    __device__ inline void load(const void *from, int tid) {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if ((i + 1) * PT <= COUNT || i * PT + tid < COUNT) x[i] = static_cast<const u32x4 *>(from)[i * PT + tid];
+    }
+    __device__ inline void store(u32x4 *to, int tid) const {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if ((i + 1) * PT <= COUNT || i * PT + tid < COUNT) to[i * PT + tid] = x[i];
+    }
 };
 
 // The producing waves: 4 DK threads; a thread takes 4 tokens x 4 channels.
@@ -77,24 +104,26 @@ template <int DK, bool KEYVEC, bool BF16, Pass PASS>
 struct Producer {
     typedef PassShared<DK, KEYVEC, BF16, PASS> Shared;
     typedef typename Raw4<BF16>::type raw;
-    static constexpr int NK = Shared::NK, NQ = Shared::NQ, TP = Shared::TP;
+    static constexpr int NK = Shared::NK, NQ = Shared::NQ;
     static constexpr int PT = 4 * DK, CG = DK / 4;           // threads; channel groups
-    static constexpr bool kQ = PASS != kSave;
+    static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse, kQ = PASS != kSave;
     raw k[4], q[kQ ? 4 : 1];
     float4 a[KEYVEC ? 4 : 1], pre, suf, sk, sq;
-    u32x4 tp0, tp1, tp2, tp3, tp4, tp5, meta;
-    half4 w[NK][4], v[PASS == kReverse ? NQ : 1][4];  // columns of the chunk whose rows are written
+    Pieces<2 * kPart, PT> tm;        // T, N' or N^T
+    Pieces<Shared::NP * kPart, PT> pm;  // P or P^T
+    u32x4 meta;
+    half4 w[NK][4];                  // K^T of the chunk whose A half is written
     int n;                           // tokens of the chunk in k, q and a
     int tid, cg, tg;
 
-    __device__ inline void load(const ChunkArgs &A, int h, int first, int n_, size_t entry) {
+    __device__ inline void fetch(const ChunkArgs &A, int h, int first, int n_, size_t entry) {
         n = n_;
         const ChunkPrep *e = A.prep + entry;
         const size_t base = ((size_t)first * A.s.H + h) * CG;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // past the last token its row again: T (N^T) has zeros in those columns and rows,
-            // so whatever finite values stand there add nothing
+            // past the last token its row again: T (N', N^T) and u have zeros there, so whatever
+            // finite values stand there add nothing
             const uint32_t at = (uint32_t)min(4 * tg + i, n - 1) * (uint32_t)(A.s.H * CG) + cg;
             k[i] = (static_cast<const raw *>(A.s.k) + base)[at];
             if constexpr (kQ) q[i] = (static_cast<const raw *>(A.s.q) + base)[at];
@@ -107,23 +136,7 @@ struct Producer {
         sk = *reinterpret_cast<const float4 *>(&e->m.sk[4 * tg]);
         if constexpr (kQ) sq = *reinterpret_cast<const float4 *>(&e->m.sq[4 * tg]);
         if (tid < kMeta) meta = reinterpret_cast<const u32x4 *>(&e->m)[tid];
-    }
-
-    // f(piece, its number) over this thread's pieces of the triangular matrices
-    template <class F>
-    __device__ inline void pieces(F f) {
-        f(tp0, tid);
-        f(tp1, tid + PT);
-        if (3 * PT <= TP || tid + 2 * PT < TP) f(tp2, tid + 2 * PT);
-        if constexpr (3 * PT < TP) f(tp3, tid + 3 * PT);
-        if constexpr (4 * PT < TP)
-            if (5 * PT <= TP || tid + 4 * PT < TP) f(tp4, tid + 4 * PT);
-        if constexpr (5 * PT < TP) f(tp5, tid + 5 * PT);
-    }
-
-    __device__ inline void load_tp(const ChunkArgs &A, size_t entry) {
-        const void *e = PASS == kReverse ? static_cast<const void *>(A.back + entry) : A.prep + entry;
-        pieces([&](u32x4 &x, int i) { x = reinterpret_cast<const u32x4 *>(e)[i]; });
+        if constexpr (REV) pm.load(A.back[entry].P, tid);
     }
 
     // Gate of the thread's token i: 1 past the last token.
@@ -133,8 +146,15 @@ struct Producer {
         for (int c = 0; c < 4; ++c) x[c] = 4 * tg + i < n ? x[c] : 1.f;
     }
 
-    // The chunk's rows into LDS, its columns into w and v.
-    __device__ inline void write_rows(Shared &sh, int which) {
+    // Where column c of the thread stands among the columns' fragments.
+    __device__ inline int column(int c, int &ct) const {
+        const int ch = 4 * cg + c;
+        ct = ch >> 4;
+        return place_w(ch & 15, tg & 3, ct) + ((tg >> 2) & 1) * 4;
+    }
+
+    // The chunk's A half into LDS, its K^T into w.
+    __device__ inline void write_a(Shared &sh, int which) {
         float before[4], after[4][4];  // gate products up to and past a token
         if constexpr (KEYVEC) {
             widen(pre, before);
@@ -153,6 +173,7 @@ struct Producer {
         }
         const int g = cg & 3, ks = cg >> 3, eh = ((cg >> 2) & 1) * 4, rt = tg >> 2;
         const float ek[4] = {sk.x, sk.y, sk.z, sk.w}, eq[4] = {sq.x, sq.y, sq.z, sq.w};
+        half4 v[REV ? NQ : 1][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float kx[4], qx[4];
@@ -170,10 +191,10 @@ struct Producer {
                 _Float16 hi, lo;
                 if constexpr (NK == 2) {
                     const float b = KEYVEC ? kx[c] * before[c] : kx[c], f = KEYVEC ? kx[c] * after[i][c] : kx[c];
-                    split(PASS == kReverse ? f : b, ek[i], hi, lo);
+                    split(REV ? f : b, ek[i], hi, lo);
                     kh[c] = hi;
                     kl[c] = lo;
-                    if constexpr (KEYVEC) split(PASS == kReverse ? b : f, ek[i], hi, lo);
+                    if constexpr (KEYVEC) split(REV ? b : f, ek[i], hi, lo);
                     w[0][c][i] = hi;
                     w[NK - 1][c][i] = lo;
                 } else {
@@ -183,7 +204,7 @@ struct Producer {
                     split(KEYVEC ? qx[c] * before[c] : qx[c], eq[i], hi, lo);
                     qh[c] = hi;
                     ql[c] = lo;
-                    if constexpr (PASS == kReverse) {
+                    if constexpr (REV) {
                         v[0][c][i] = hi;
                         if constexpr (NQ == 2) v[NQ - 1][c][i] = lo;
                     }
@@ -192,50 +213,67 @@ struct Producer {
             const int at = place_k(4 * (tg & 3) + i, g, ks) + eh;
             *reinterpret_cast<half4 *>(&sh.K[0][rt][ks][at]) = kh;
             if constexpr (NK == 2) *reinterpret_cast<half4 *>(&sh.K[NK - 1][rt][ks][at]) = kl;
-            if constexpr (PASS == kForward) {
+            if constexpr (FWD) {
                 *reinterpret_cast<half4 *>(&sh.Q[0][rt][ks][at]) = qh;
                 if constexpr (NQ == 2) *reinterpret_cast<half4 *>(&sh.Q[NQ - 1][rt][ks][at]) = ql;
             }
         }
-        if (tid < kMeta) reinterpret_cast<u32x4 *>(&sh.m[which])[tid] = meta;
-    }
-
-    __device__ inline void write_columns(Shared &sh) {
+        if constexpr (REV) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int ch = 4 * cg + c, ct = ch >> 4;
-            const int at = place_w(ch & 15, tg & 3, ct) + ((tg >> 2) & 1) * 4;
-#pragma unroll
-            for (int l = 0; l < NK; ++l) *reinterpret_cast<half4 *>(&sh.W[l][ct][tg >> 3][at]) = w[l][c];
-            if constexpr (PASS == kReverse) {
+            for (int c = 0; c < 4; ++c) {
+                int ct;
+                const int at = column(c, ct);
 #pragma unroll
                 for (int l = 0; l < NQ; ++l) *reinterpret_cast<half4 *>(&sh.V[l][ct][tg >> 3][at]) = v[l][c];
             }
+            pm.store(sh.P, tid);
         }
-        pieces([&](u32x4 &x, int i) { sh.tp[i] = x; });
+        if (tid < kMeta) reinterpret_cast<u32x4 *>(&sh.m[which])[tid] = meta;
+    }
+
+    __device__ inline void write_b(Shared &sh) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            int ct;
+            const int at = column(c, ct);
+#pragma unroll
+            for (int l = 0; l < NK; ++l) *reinterpret_cast<half4 *>(&sh.W[l][ct][tg >> 3][at]) = w[l][c];
+        }
+        tm.store(sh.T, tid);
     }
 
     // All of a producing thread's work on a sequence of nc chunks: step i is chunk i, or nc - 1 - i
-    // in the reverse pass.
-    __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry) {
+    // in the reverse pass.  The forward pass has a last step for the outputs of the chunk before.
+    __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry0) {
         cg = tid % CG;
         tg = tid / CG;
-        auto chunk = [&](int i) { return PASS == kReverse ? nc - 1 - i : i; };
-        auto fetch = [&](int i) {
+        auto chunk = [&](int i) { return REV ? nc - 1 - i : i; };
+        auto entry = [&](int i) { return entry0 + (size_t)chunk(i) * A.s.H; };
+        auto get = [&](int i) {
             const int c = chunk(i);
-            load(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry + (size_t)c * A.s.H);
+            fetch(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry(i));
         };
-        fetch(0);
-        load_tp(A, entry + (size_t)chunk(0) * A.s.H);
-        write_rows(sh, 0);
-        if (nc > 1) fetch(1);
-        for (int i = 0; i < nc; ++i) {
-            lds_barrier();               // the rows of i stand; matrices and columns of i - 1 are done with
-            write_columns(sh);
-            if (i + 1 < nc) load_tp(A, entry + (size_t)chunk(i + 1) * A.s.H);
-            lds_barrier();               // matrices and columns of i stand; the rows of i are done with
-            if (i + 1 < nc) write_rows(sh, (i + 1) & 1);
-            if (i + 2 < nc) fetch(i + 2);
+        auto get_t = [&](int i) {
+            if constexpr (REV) tm.load(A.back[entry(i)].N, tid);
+            else tm.load(A.prep[entry(i)].T, tid);
+        };
+        get(0);
+        get_t(0);
+        write_a(sh, 0);
+        if (nc > 1) get(1);
+        int which = 0;
+        for (int i = 0; i < nc + (FWD ? 1 : 0); ++i) {
+            lds_barrier();               // half A of i stands; half B of i - 1 is done with
+            if (i < nc) write_b(sh);
+            if constexpr (FWD)
+                if (i > 0) pm.store(sh.P, tid);
+            if (i + 1 < nc) get_t(i + 1);
+            if constexpr (FWD)
+                if (i < nc) pm.load(A.prep[entry(i)].P, tid);
+            lds_barrier();               // half B of i stands; half A of i is done with
+            which = which == 2 ? 0 : which + 1;
+            if (i + 1 < nc) write_a(sh, which);
+            if (i + 2 < nc) get(i + 2);
         }
     }
 };
@@ -299,6 +337,78 @@ __device__ inline void mul4(const half8 (&f)[4], half8 x, floatx4 (&Y)[4], int f
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (i >= first) Y[i] = mfma16(f[i], x, Y[i]);
+}
+
+// Blocks of four row tiles through all k steps: Y += (K hi + K lo) (x hi + x lo), rows KS * kFrag apart,
+// K lo 4 rows further.  `place` gives the fragments of a k step, `operand` the right
+// operand.
+template <int KS, int NK, class P, class O>
+__device__ inline void rows_times(P place, O operand, floatx4 (&Y)[4], half8 (&f)[4], half8 (&f2)[4]) {
+    constexpr int row = KS * kFrag;
+    half8 hi, lo;
+    operand(0, hi, lo);
+    lds_half at = place(0);
+    load4(f, at, row);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const lds_half now = at;
+        half8(&x0)[4] = NK == 1 && (ks & 1) ? f2 : f;
+        half8(&x1)[4] = NK == 1 && (ks & 1) ? f : f2;
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (NK == 2) load4(x1, now + 4 * row, row);
+        if (ks + 1 < KS) at = place(ks + 1);
+        if constexpr (NK == 1)
+            if (ks + 1 < KS) load4(x1, at, row);
+        mul4(x0, hi, Y);
+        mul4(x0, lo, Y);
+        if constexpr (NK == 2) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (ks + 1 < KS) load4(x0, at, row);
+            mul4(x1, hi, Y);
+        }
+        if (ks + 1 < KS) operand(ks + 1, hi, lo);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A state's tile, or another's, as it stands in the registers: [tile][lane][4].
+__device__ inline void store_tiles(float *to, const floatx4 *x, int n) {
+    floatx4 *p = reinterpret_cast<floatx4 *>(to) + (threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[64 * i] = x[i];
+}
+
+// Columns of (K^T hi + K^T lo) (x hi + x lo): tile by tile, each given to `done`.  f: on entry
+// the first block, on its way.
+template <int CT, int NK, class L, class D>
+__device__ inline void columns_times(L load, const half8 (&hi)[2], const half8 (&lo)[2], half8 (&f)[4], half8 (&f2)[4],
+                                     D done) {
+#pragma unroll
+    for (int c0 = 0; c0 < CT; c0 += 4) {
+        floatx4 z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            __builtin_amdgcn_sched_barrier(0);
+            const bool more = ks == 0 || c0 + 4 < CT;
+            const int nc0 = ks ? c0 + 4 : c0, nks = ks ? 0 : 1;
+            if constexpr (NK == 2) {
+                load(f2, 1, c0, ks);
+                mul4(f, hi[ks], z);
+                mul4(f, lo[ks], z);
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) load(f, 0, nc0, nks);
+                mul4(f2, hi[ks], z);
+            } else {
+                if (more) load(ks ? f : f2, 0, nc0, nks);
+                mul4(ks ? f2 : f, hi[ks], z);
+                mul4(ks ? f2 : f, lo[ks], z);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) done(c0 + i, z[i]);
+    }
 }
 
 // A lower triangular left operand (fragments at t, lo parts kTri further) times

@@ -123,7 +123,7 @@ __device__ inline void store_pt(const floatx4 (&p)[4], float (*tm)[kC], ChunkMet
     __syncthreads();
 }
 
-// Row w of P's blocks (backward: of A's).
+// Row w of P's blocks.
 __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
     const int lane = threadIdx.x & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
     floatx4 s, inv;
@@ -141,11 +141,9 @@ __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
     if (c16 == 0) *reinterpret_cast<floatx4 *>(&out.m.rp[16 * w + 4 * g]) = inv;
 }
 
-// From M = diag(beta) A in LDS (strictly lower; what lies above the diagonal is
-// not read) to T.
-template <bool BACK>
-__device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)[kC], const float *be, ChunkPrep &out,
-                               ChunkBack *back) {
+// Block column `wave` of the inverse of I + M, M strictly lower triangular in LDS (what lies above
+// the diagonal is not read).
+__device__ inline void invert(const float (*M)[LD], float (*X)[20], floatx4 (&t)[4]) {
     const int lane = threadIdx.x & 63, wave = wave_index(), j = lane & 15, g = lane >> 4;
     // inverse of the diagonal block `wave`, column j
     float x[16];
@@ -166,7 +164,6 @@ __device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)
         for (int i = 0; i < 16; ++i) X[16 * wave + i][j] = x[i];
     }
     __syncthreads();
-    floatx4 t[4];  // blocks of column `wave`
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
         if (I < wave) {
@@ -189,6 +186,16 @@ __device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)
             t[I] = z;
         }
     }
+}
+
+// From M = diag(beta) A in LDS to T; backward: to N^T, and from A diag(beta), written over M, to
+// N' = (I + A diag(beta))^-1, which takes R to the delta errors w, in T's place.
+template <bool BACK>
+__device__ inline void store_t(float (*M)[LD], float (*X)[20], float (*tm)[kC], const float *be, const floatx4 (&A)[4],
+                               ChunkPrep &out, ChunkBack *back) {
+    const int lane = threadIdx.x & 63, wave = wave_index(), j = lane & 15, g = lane >> 4;
+    floatx4 t[4];
+    invert(M, X, t);
     const float b = be[16 * wave + j];
     if constexpr (BACK) {
         float m = 0.f, inv;
@@ -204,13 +211,21 @@ __device__ inline void store_t(const float (*M)[LD], float (*X)[20], float (*tm)
             out.m.rn[16 * wave + j] = inv;
             out.m.be[16 * wave + j] = b;
         }
+        __syncthreads();
+#pragma unroll
+        for (int J = 0; J < 4; ++J)
+            if (J <= wave)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) M[16 * wave + 4 * g + r][16 * J + j] = A[J][r] * be[16 * J + j];
+        __syncthreads();
+        invert(M, X, t);
     }
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
         floatx4 m;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            t[I][r] *= b;
+            if constexpr (!BACK) t[I][r] *= b;
             m[r] = max_row(fabsf(t[I][r]));
         }
         if (j == 0) *reinterpret_cast<floatx4 *>(&tm[wave][16 * I + 4 * g]) = m;
@@ -251,7 +266,7 @@ __device__ inline void order_sequences(const ChunkArgs &A, int *len) {
     }
 }
 
-// BACK: what the backward pass reads (A in P's place, N^T and P^T).
+// BACK: what the backward pass reads (N' in T's place, N^T and P^T).
 template <int DK, bool BF16, bool BACK>
 __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     constexpr int KS = DK / 32;
@@ -362,12 +377,11 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     if constexpr (BACK) {
         back = A.back + (size_t)slot * s.H + h;
         store_pt(pp, tm, out.m, *back);
-        store_p(aa, out);
     } else {
         store_p(pp, out);
     }
     __syncthreads();
-    store_t<BACK>(big.M, X, tm, be, out, back);
+    store_t<BACK>(big.M, X, tm, be, aa, out, back);
 }
 
 template <int DK, bool BF16, bool BACK>
@@ -587,12 +601,11 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
     if constexpr (BACK) {
         back = A.back + (size_t)slot * s.H + h;
         store_pt(pp, tm, out.m, *back);
-        store_p(aa, out);
     } else {
         store_p(pp, out);
     }
     __syncthreads();
-    store_t<BACK>(big.M, X, tm, be, out, back);
+    store_t<BACK>(big.M, X, tm, be, aa, out, back);
 }
 
 template <int DK, bool BACK>

@@ -6,9 +6,9 @@
 //   dS = diag(G_64) dS + (Q G)^T dO - (K G)^T (beta y).
 // The gradient behind each chunk and y are kept for the chunk's own gradients.
 //
-// Laid out as the pass of the state (stq_chunk_fwd.hip): a wave owns 16 columns of dS in its
-// registers, the left operands come from LDS, where the producing waves replace one
-// half's while the other half multiplies.
+// Laid out as the pass of the state (stq_chunk_fwd.hip).  The chain from one dS to the next is du,
+// y, dS; the helping waves form what does not depend on it, P^T dO and (Q G)^T dO, and hand it
+// over as result tiles in LDS.
 #include <type_traits>
 
 #include "stq_chunk_pass.h"
@@ -56,11 +56,12 @@ __device__ inline void upper(lds_half t, const floatx4 (&X)[4], floatx4 (&Y)[4],
 }
 
 template <int DK, int DV, bool KEYVEC, bool BF16>
-__global__ void __launch_bounds__(256 + 4 * DK) k_chunk_rev(const ChunkArgs A) {
+__global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kReverse>::NW + 4 * DK))
+    k_chunk_rev(const ChunkArgs A) {
     typedef PassShared<DK, KEYVEC, BF16, kReverse> Shared;
     typedef typename Raw4<BF16>::type raw;
-    constexpr int KS = Shared::KS, CT = Shared::CT, NK = Shared::NK, NQ = Shared::NQ;
-    constexpr int parts = DV / 64;       // workgroups of a (sequence, head)
+    constexpr int KS = Shared::KS, CT = Shared::CT, NK = Shared::NK, NQ = Shared::NQ, NW = Shared::NW;
+    constexpr int parts = DV / (16 * NW);  // workgroups of a (sequence, head)
     __shared__ Shared sh;
     const int H = A.s.H;
     uint32_t seq, at_seq;
@@ -70,17 +71,84 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_rev(const ChunkArgs A) {
     seq_range(A.s, b, t0, t1);
     const int nc = (t1 - t0 + kC - 1) / kC;
     const size_t entry0 = (size_t)(t0 / kC + b) * H + h;
+    const int wave = wave_index();
 
-    if (threadIdx.x >= 256) {
+    if (wave >= 2 * NW) {
         if (nc == 0) return;
         Producer<DK, KEYVEC, BF16, kReverse> p;
-        p.tid = threadIdx.x - 256;
+        p.tid = threadIdx.x - 64 * 2 * NW;
         p.run(A, sh, h, t0, t1, nc, entry0);
         return;
     }
 
-    const int lane = threadIdx.x & 63, wave = wave_index(), c16 = lane & 15, g = lane >> 4;
-    const int col0 = (part * 4 + wave) * 16;
+    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4, mine = wave < NW ? wave : wave - NW;
+    const int col0 = (part * NW + mine) * 16;
+    // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
+    const int row0 = 4 * g + (c16 & 3);
+    const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
+    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
+    half8 f[4], f2[4];
+    int which = 0;
+
+    if (wave >= NW) {                    // what dO gives to 16 columns
+        if (nc == 0) return;
+        raw v[4];                        // dO of the next chunk
+        auto load_v = [&](int c) {
+            const raw *base = static_cast<const raw *>(A.dout) + (size_t)(t0 + c * kC) * row_step + col4;
+            const int n = t1 - t0 - c * kC;
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + row0, n - 1) * row_step];
+        };
+        load_v(nc - 1);
+        for (int i = 0; i < nc; ++i) {
+            const int c = nc - 1 - i, n = t1 - t0 - c * kC;
+            floatx4 D[4], y[4];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                float x[4];
+                widen(v[rt], x);
+                const bool on = 16 * rt + row0 < n;  // past the last token: 0
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = on ? x[r] : 0.f;
+                quad_transpose(x);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) D[rt][r] = x[r];
+            }
+            if (c > 0) load_v(c - 1);
+            lds_barrier();
+            const lds_float m = float_at(&sh.m[which], 4 * g);
+            float undo;
+            upper<!BF16>(half_at(&sh.P, lane * 8), D, y, undo);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const floatx4 x = row_factors(m + factors(offsetof(ChunkMeta, rpt), rt)),
+                              rq = row_factors(m + factors(offsetof(ChunkMeta, rq), rt));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    y[rt][r] = (y[rt][r] * x[r]) * undo;
+                    D[rt][r] *= rq[r];
+                }
+                sh.pd[mine][rt][lane] = y[rt];
+            }
+            const float sd = scale_to(column_max(D), 13, undo);
+            half8 dh[2], dl[2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) right(D[2 * ks], D[2 * ks + 1], sd, dh[ks], dl[ks]);
+            lds_half vb[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) vb[j] = half_at(&sh.V, place_w(c16, g, j));
+            auto load_c = [&](half8 (&x)[4], int l, int c0, int ks) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = frag(vb[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
+            };
+            load_c(f, 0, 0, 0);
+            columns_times<CT, NQ>(load_c, dh, dl, f, f2, [&](int ct, floatx4 z) { sh.zd[mine][ct][lane] = z * undo; });
+            lds_barrier();
+            which = which == 2 ? 0 : which + 1;
+        }
+        return;
+    }
+
     floatx4 S[CT];
     const size_t state0 = ((size_t)b * H + h) * DK * DV + col0;
     uint32_t at0 = 4 * g * DV + c16;     // of the lane's first value in the state
@@ -90,168 +158,66 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_rev(const ChunkArgs A) {
         for (int r = 0; r < 4; ++r) S[ct][r] = A.dlast ? (A.dlast + state0 + (16 * ct + r) * DV)[at0] : 0.f;
     asm volatile("" : "+v"(at0));
 
-    // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
-    const int row0 = 4 * g + (c16 & 3);
-    const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
-    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
-    raw v[4];                            // dO of the next chunk
-    auto load_v = [&](int c) {
-        const raw *base = static_cast<const raw *>(A.dout) + (size_t)(t0 + c * kC) * row_step + col4;
-        const int n = t1 - t0 - c * kC;
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + row0, n - 1) * row_step];
-    };
-    if (nc) load_v(nc - 1);
-
     for (int i = 0; i < nc; ++i) {
         const int c = nc - 1 - i, n = t1 - t0 - c * kC;
         const size_t entry = entry0 + (size_t)c * H;
-        {
-            float *to = A.dS + entry * (DK * DV) + col0;
-            uint32_t at = 4 * g * DV + c16;
-            asm volatile("" : "+v"(at));
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) (to + (16 * ct + r) * DV)[at] = S[ct][r];
-        }
-        floatx4 R[4], D[4], y[4];
+        store_tiles(A.dS + entry * (DK * DV) + col0 * DK, S, CT);
+        floatx4 R[4], y[4];
         float undo;
         const float s = scale_to(column_max(S), 13, undo);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) R[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
-        half8 hi, lo, f[4], f2[4];
-        right(S[0], S[1], s, hi, lo);
         lds_barrier();
-        const lds_float m = float_at(&sh.m[i & 1], 4 * g);
-        auto place = [&](int ks) { return half_at(&sh.K, place_k(c16, g, ks)) + ks * kFrag; };
-        lds_half kq = place(0);
-        constexpr int row = KS * kFrag;  // step to the next row tile
-        load4(f, kq, row);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const lds_half now = kq;
-            half8(&x0)[4] = NK == 1 && (ks & 1) ? f2 : f;
-            half8(&x1)[4] = NK == 1 && (ks & 1) ? f : f2;
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (NK == 2) load4(x1, now + 4 * row, row);
-            if (ks + 1 < KS) kq = place(ks + 1);
-            if constexpr (NK == 1)
-                if (ks + 1 < KS) load4(x1, kq, row);
-            mul4(x0, hi, R);
-            mul4(x0, lo, R);
-            if constexpr (NK == 2) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (ks + 1 < KS) load4(x0, kq, row);
-                mul4(x1, hi, R);
-            }
-            if (ks + 1 < KS) right(S[2 * ks + 2], S[2 * ks + 3], s, hi, lo);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        const lds_float m = float_at(&sh.m[which], 4 * g);
+        rows_times<KS, NK>([&](int ks) { return half_at(&sh.K, place_k(c16, g, ks)) + ks * kFrag; },
+                           [&](int ks, half8 &hi, half8 &lo) { right(S[2 * ks], S[2 * ks + 1], s, hi, lo); }, R, f, f2);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             const floatx4 rw = row_factors(m + factors(offsetof(ChunkMeta, rw), rt));
-            float x[4];
-            widen(v[rt], x);
-            const bool on = 16 * rt + row0 < n;  // past the last token: 0
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = on ? x[r] : 0.f;
-            quad_transpose(x);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                D[rt][r] = x[r];
-                R[rt][r] = (R[rt][r] * rw[r]) * undo;
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < 4; ++r) R[rt][r] = (R[rt][r] * rw[r]) * undo;
         }
-        if (c > 0) load_v(c - 1);
         lds_barrier();
-        const lds_half t = half_at(&sh.tp, lane * 8);
-        upper<!BF16>(t + 2 * kTri * kFrag, D, y, undo);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            const floatx4 x = row_factors(m + factors(offsetof(ChunkMeta, rpt), rt));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[rt][r] = __builtin_fmaf(y[rt][r] * x[r], undo, R[rt][r]);
-        }
-        upper<true>(t, R, y, undo);
-        float4 *ys = reinterpret_cast<float4 *>(A.y) + entry * (kC * DV / 4) + col0 / 4 + (c16 >> 2);
+        for (int rt = 0; rt < 4; ++rt) R[rt] += sh.pd[mine][rt][lane];
+        upper<true>(half_at(&sh.T, lane * 8), R, y, undo);
         raw *dv = static_cast<raw *>(A.dv) + (size_t)(t0 + c * kC) * row_step + col4;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             const floatx4 rn = row_factors(m + factors(offsetof(ChunkMeta, rn), rt)),
                           be = row_factors(m + factors(offsetof(ChunkMeta, be), rt)),
-                          rk = row_factors(m + factors(offsetof(ChunkMeta, rk), rt)),
-                          rq = row_factors(m + factors(offsetof(ChunkMeta, rq), rt));
-            float x[4], z[4];
+                          rk = row_factors(m + factors(offsetof(ChunkMeta, rk), rt));
+            float z[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                x[r] = (y[rt][r] * rn[r]) * undo;
-                z[r] = be[r] * x[r];
+                y[rt][r] = (y[rt][r] * rn[r]) * undo;
+                z[r] = be[r] * y[rt][r];
                 R[rt][r] = -z[r] * rk[r];
-                D[rt][r] *= rq[r];
             }
-            quad_transpose(x);
             quad_transpose(z);
-            ys[(16 * rt + row0) * (DV / 4)] = make_float4(x[0], x[1], x[2], x[3]);
             raw out;
             narrow(z, out);
             if (16 * rt + row0 < n) dv[(uint32_t)(16 * rt + row0) * row_step] = out;
-            __builtin_amdgcn_sched_barrier(0);
         }
-        // both column blocks under one scale, for sums in the same registers
-        const float su = scale_to(fmaxf(column_max(R), column_max(D)), 13, undo);
-        half8 kh[2], kl[2], qh[2], ql[2];
+        store_tiles(A.y + entry * (kC * DV) + col0 * kC, y, 4);
+        const float su = scale_to(column_max(R), 13, undo);
+        half8 kh[2], kl[2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            right(R[2 * ks], R[2 * ks + 1], su, kh[ks], kl[ks]);
-            right(D[2 * ks], D[2 * ks + 1], su, qh[ks], ql[ks]);
-        }
-        lds_half wb[4], vb[4];
+        for (int ks = 0; ks < 2; ++ks) right(R[2 * ks], R[2 * ks + 1], su, kh[ks], kl[ks]);
+        lds_half wb[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            wb[j] = half_at(&sh.W, place_w(c16, g, j));
-            vb[j] = half_at(&sh.V, place_w(c16, g, j));
-        }
-        auto load_c = [&](half8 (&x)[4], const lds_half (&from)[4], int l, int c0, int ks) {
+        for (int j = 0; j < 4; ++j) wb[j] = half_at(&sh.W, place_w(c16, g, j));
+        auto load_w = [&](half8 (&x)[4], int l, int c0, int ks) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = frag(from[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
+            for (int j = 0; j < 4; ++j) x[j] = frag(wb[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
         };
-        load_c(f, wb, 0, 0, 0);
+        load_w(f, 0, 0, 0);
+        columns_times<CT, NK>(load_w, kh, kl, f, f2, [&](int ct, floatx4 z) {
+            const floatx4 d = row_factors(m + factors(offsetof(ChunkMeta, dec), ct)), q = sh.zd[mine][ct][lane];
 #pragma unroll
-        for (int c0 = 0; c0 < CT; c0 += 4) {
-            floatx4 z[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bool more = ks == 0 || c0 + 4 < CT;
-                const int nc0 = ks ? c0 + 4 : c0, nks = ks ? 0 : 1;
-                __builtin_amdgcn_sched_barrier(0);
-                load_c(f2, vb, 0, c0, ks);
-                mul4(f, kh[ks], z);
-                mul4(f, kl[ks], z);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (NK == 2) load_c(f, wb, 1, c0, ks);
-                else if (more) load_c(f, wb, 0, nc0, nks);
-                mul4(f2, qh[ks], z);
-                mul4(f2, ql[ks], z);
-                if constexpr (NK == 2) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    load_c(f2, vb, NQ - 1, c0, ks);
-                    mul4(f, kh[ks], z);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (more) load_c(f, wb, 0, nc0, nks);
-                    mul4(f2, qh[ks], z);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const floatx4 d = row_factors(m + factors(offsetof(ChunkMeta, dec), c0 + j));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[c0 + j][r] = __builtin_fmaf(z[j][r], undo, S[c0 + j][r] * d[r]);
-            }
-        }
+            for (int r = 0; r < 4; ++r) S[ct][r] = __builtin_fmaf(z[r], undo, __builtin_fmaf(S[ct][r], d[r], q[r]));
+        });
+        which = which == 2 ? 0 : which + 1;
     }
     if (!A.dinitial) return;
 #pragma unroll
@@ -260,14 +226,19 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_rev(const ChunkArgs A) {
         for (int r = 0; r < 4; ++r) (A.dinitial + state0 + (16 * ct + r) * DV)[at0] = S[ct][r];
 }
 
+template <int DK, int DV, bool KEYVEC, bool BF16>
+void go(const ChunkArgs &a, hipStream_t s) {
+    constexpr int NW = PassShared<DK, KEYVEC, BF16, kReverse>::NW;
+    const dim3 grid((unsigned)(DV / (16 * NW)) * (unsigned)a.s.H * (unsigned)a.s.B);
+    k_chunk_rev<DK, DV, KEYVEC, BF16><<<grid, 64 * 2 * NW + 4 * DK, 0, s>>>(a);
+}
+
 template <int DK, int DV>
 void go(const ChunkArgs &a, bool keyvec, bool bf16, hipStream_t s) {
-    const dim3 grid((unsigned)(DV / 64) * (unsigned)a.s.H * (unsigned)a.s.B);
-    constexpr int block = 256 + 4 * DK;
-    if (keyvec && bf16) k_chunk_rev<DK, DV, true, true><<<grid, block, 0, s>>>(a);
-    else if (keyvec) k_chunk_rev<DK, DV, true, false><<<grid, block, 0, s>>>(a);
-    else if (bf16) k_chunk_rev<DK, DV, false, true><<<grid, block, 0, s>>>(a);
-    else k_chunk_rev<DK, DV, false, false><<<grid, block, 0, s>>>(a);
+    if (keyvec && bf16) go<DK, DV, true, true>(a, s);
+    else if (keyvec) go<DK, DV, true, false>(a, s);
+    else if (bf16) go<DK, DV, false, true>(a, s);
+    else go<DK, DV, false, false>(a, s);
 }
 
 }  // namespace
