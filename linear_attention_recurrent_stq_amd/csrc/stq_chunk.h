@@ -68,6 +68,10 @@ struct ChunkArgs {
     ChunkGates *gates;               // the same, key-vector gates only
     int32_t slots;                   // chunk slots: N / 64 + B
     int32_t *order;                  // [B] sequences, longest first, or nullptr: as they come
+    // Sequences cut into `segs` segments (chunk_segments; 1: they are not), per (sequence, head)
+    int32_t segs;
+    float *steps;                    // [segs - 1][d_k][d_v + d_k]: a segment's end from no state | its matrix
+    float *starts;                   // [segs][d_k][d_v]: the state before each segment
     // The backward pass (back not nullptr): per (chunk, head)
     ChunkBack *back;
     float *S, *dS;                   // first state; gradient of the last one [d_k,d_v]
@@ -85,7 +89,30 @@ constexpr int kOrdered = 1024;       // sequences that are put in order of lengt
 // different chunks differ, and none reaches N / 64 + B.
 inline int chunk_slots(int N, int B) { return N / kC + B; }
 
+// Few long sequences leave most of the 256 CUs without work, for a pass goes through a
+// sequence's chunks in turn.  Then each is cut into segments, and the state passes through
+// all of them at once, from no state, and so do the unit vectors of the state's rows, which
+// gives the segment's matrix (columns never meet, so those are d_k columns more); the states
+// before the segments follow, one small product each, and then the outputs of all segments at once.
+// That is twice the work and d_k columns more, so it is done where all of it runs side by
+// side, one workgroup a CU, in segments of at least kSegment chunks: from 3 segments on
+// (2 of them take as long as none: each half twice).
+constexpr int kSegment = 16;
+inline int chunk_segments(int H, int dk, int dv, int B, int N) {
+    const int64_t heads = (int64_t)B * H;
+    for (int s = B > 0 ? (N / kC / B / kSegment < 16 ? N / kC / B / kSegment : 16) : 1; s > 2; --s)
+        if (heads * ((s - 1) * (dv / 64) + (s - 2) * (dk / 64)) <= 256) return s;
+    return 1;
+}
+// No call with at most N tokens has more (sequence, head, segment) triples that are not a
+// sequence's last: heads * (s - 1) stays under both.
+inline int64_t chunk_steps(int H, int dv, int N) {
+    const int64_t a = 256 / (dv / 64), b = (int64_t)H * (N / kC / kSegment);
+    return a < b ? a : b;
+}
+
 hipError_t launch_chunk_prep(const ChunkArgs &a, int dk, bool keyvec, bool bf16, hipStream_t s);
+// (through segments where a.segs > 1)
 hipError_t launch_chunk_forward(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);
 
 hipError_t launch_chunk_reverse(const ChunkArgs &a, int dk, int dv, bool keyvec, bool bf16, hipStream_t s);

@@ -47,37 +47,34 @@ __device__ inline void narrow(const float (&x)[4], float4 &w) { w = make_float4(
 // The passes over a sequence's chunks.  Every chunk (step i) has two halves, A and B, parted by
 // barriers; what one half reads is replaced while the other half runs:
 //   forward: A reads K, Q [token x channel] times the gates up to a token (before);
-//            B reads K^T [channel x token] times those after it, T, and P of the step before
-//   save:    A K before; B K^T after, N' (in T's place).  Leaves each chunk's first state and delta
-//            errors w, which the backward pass starts from
+//            B reads K^T [channel x token] times those after it, T and P
+//   carry:   A K before; B K^T after, T.  The state alone, no outputs
+//   save:    as carry, N' in T's place.  Leaves each chunk's first state and delta errors w, which
+//            the backward pass starts from
 //   reverse: A K after, Q^T before, P^T; B K^T before, N^T.  The state's gradient, last chunk first
-enum Pass { kForward, kSave, kReverse };
+enum Pass { kForward, kCarry, kSave, kReverse };
 
 // What a rule's operands carry.  All that a state or its gradient depends on keeps 22 bits:
 // K (and Q^T) in the hi part alone where the rows are bf16 and not folded with gates.  Q and P of
 // the forward pass reach the outputs only; for bf16 outputs (half a step: 2^-9) their hi
 // parts, and those of what they multiply, are enough (2^-12).
 //
-// NW: columns of 16 of a workgroup, each with a wave that carries the state and (forward, reverse) one
-// that helps it: four, or two where the fragments of four do not fit in LDS.
+// NW: columns of 16 of a workgroup, each with a wave that carries the state and (reverse) one that
+// helps it: four, or two where what the helpers hand over leaves no room for four in LDS.
 template <int DK, bool KEYVEC, bool BF16, Pass PASS>
 struct PassShared {
     static constexpr int NK = KEYVEC || !BF16 ? 2 : 1, KS = DK / 32, CT = DK / 16;
     static constexpr int NQ = PASS == kForward ? (BF16 ? 1 : 2) : NK;  // parts of Q
     static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (P^T)
     static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse;
-    static constexpr int NW = DK == 128 && ((FWD && !BF16) || (REV && NK == 2)) ? 2 : 4;
-    static constexpr int NH = PASS == kSave ? 0 : NW;                  // helping waves
+    static constexpr int NW = DK == 128 && REV && NK == 2 ? 2 : 4;
     _Float16 K[NK][4][KS][kFrag];
     _Float16 Q[FWD ? NQ : 1][FWD ? 4 : 1][FWD ? KS : 1][kFrag];
     u32x4 T[2 * kPart];                          // T, N' or N^T
-    u32x4 P[PASS == kSave ? 1 : NP * kPart];     // P or P^T
-    ChunkMeta m[3];                              // of three steps in turn
+    u32x4 P[FWD || REV ? NP * kPart : 1];        // P or P^T
+    ChunkMeta m[2];                              // of even and of odd steps
     _Float16 W[NK][CT][2][kFrag];                // K^T
     _Float16 V[REV ? NQ : 1][REV ? CT : 1][REV ? 2 : 1][kFrag];  // Q^T
-    // forward, carrier to helper: the state and u as right operands, and what undoes their scales
-    _Float16 sf[FWD ? NQ : 1][FWD ? NW : 1][FWD ? KS : 1][kFrag], uf[FWD ? NQ : 1][FWD ? NW : 1][FWD ? 2 : 1][kFrag];
-    float us[NW][16], uu[NW][16];
     // reverse, helper to carrier: P^T dO and (Q before)^T dO, as result tiles
     floatx4 pd[REV ? NW : 1][4][REV ? 64 : 1], zd[REV ? NW : 1][REV ? CT : 1][REV ? 64 : 1];
 };
@@ -106,7 +103,7 @@ struct Producer {
     typedef typename Raw4<BF16>::type raw;
     static constexpr int NK = Shared::NK, NQ = Shared::NQ;
     static constexpr int PT = 4 * DK, CG = DK / 4;           // threads; channel groups
-    static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse, kQ = PASS != kSave;
+    static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse, kQ = FWD || REV;
     raw k[4], q[kQ ? 4 : 1];
     float4 a[KEYVEC ? 4 : 1], pre, suf, sk, sq;
     Pieces<2 * kPart, PT> tm;        // T, N' or N^T
@@ -240,10 +237,11 @@ struct Producer {
             for (int l = 0; l < NK; ++l) *reinterpret_cast<half4 *>(&sh.W[l][ct][tg >> 3][at]) = w[l][c];
         }
         tm.store(sh.T, tid);
+        if constexpr (FWD) pm.store(sh.P, tid);
     }
 
     // All of a producing thread's work on a sequence of nc chunks: step i is chunk i, or nc - 1 - i
-    // in the reverse pass.  The forward pass has a last step for the outputs of the chunk before.
+    // in the reverse pass.
     __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry0) {
         cg = tid % CG;
         tg = tid / CG;
@@ -256,23 +254,18 @@ struct Producer {
         auto get_t = [&](int i) {
             if constexpr (REV) tm.load(A.back[entry(i)].N, tid);
             else tm.load(A.prep[entry(i)].T, tid);
+            if constexpr (FWD) pm.load(A.prep[entry(i)].P, tid);
         };
         get(0);
         get_t(0);
         write_a(sh, 0);
         if (nc > 1) get(1);
-        int which = 0;
-        for (int i = 0; i < nc + (FWD ? 1 : 0); ++i) {
+        for (int i = 0; i < nc; ++i) {
             lds_barrier();               // half A of i stands; half B of i - 1 is done with
-            if (i < nc) write_b(sh);
-            if constexpr (FWD)
-                if (i > 0) pm.store(sh.P, tid);
+            write_b(sh);
             if (i + 1 < nc) get_t(i + 1);
-            if constexpr (FWD)
-                if (i < nc) pm.load(A.prep[entry(i)].P, tid);
             lds_barrier();               // half B of i stands; half A of i is done with
-            which = which == 2 ? 0 : which + 1;
-            if (i + 1 < nc) write_a(sh, which);
+            if (i + 1 < nc) write_a(sh, (i + 1) & 1);
             if (i + 2 < nc) get(i + 2);
         }
     }
@@ -359,11 +352,13 @@ __device__ inline void rows_times(P place, O operand, floatx4 (&Y)[4], half8 (&f
         if (ks + 1 < KS) at = place(ks + 1);
         if constexpr (NK == 1)
             if (ks + 1 < KS) load4(x1, at, row);
+        __builtin_amdgcn_sched_barrier(0);
         mul4(x0, hi, Y);
         mul4(x0, lo, Y);
         if constexpr (NK == 2) {
             __builtin_amdgcn_sched_barrier(0);
             if (ks + 1 < KS) load4(x0, at, row);
+            __builtin_amdgcn_sched_barrier(0);
             mul4(x1, hi, Y);
         }
         if (ks + 1 < KS) operand(ks + 1, hi, lo);
@@ -395,13 +390,16 @@ __device__ inline void columns_times(L load, const half8 (&hi)[2], const half8 (
             const int nc0 = ks ? c0 + 4 : c0, nks = ks ? 0 : 1;
             if constexpr (NK == 2) {
                 load(f2, 1, c0, ks);
+                __builtin_amdgcn_sched_barrier(0);
                 mul4(f, hi[ks], z);
                 mul4(f, lo[ks], z);
                 __builtin_amdgcn_sched_barrier(0);
                 if (more) load(f, 0, nc0, nks);
+                __builtin_amdgcn_sched_barrier(0);
                 mul4(f2, hi[ks], z);
             } else {
                 if (more) load(ks ? f : f2, 0, nc0, nks);
+                __builtin_amdgcn_sched_barrier(0);
                 mul4(ks ? f2 : f, hi[ks], z);
                 mul4(ks ? f2 : f, lo[ks], z);
             }
@@ -435,17 +433,22 @@ __device__ inline void lower(lds_half t, const floatx4 (&X)[4], floatx4 (&Y)[4],
     };
     if constexpr (FULL) {
         load(f2, kTri);
+        __builtin_amdgcn_sched_barrier(0);
         mul4(f, hi, Y);
         mul4(f, lo, Y);
         __builtin_amdgcn_sched_barrier(0);
-        right(X[2], X[3], s, hi1, lo1);
         load1(f, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        right(X[2], X[3], s, hi1, lo1);
         mul4(f2, hi, Y);
         __builtin_amdgcn_sched_barrier(0);
         load1(f2, kTri);
+        __builtin_amdgcn_sched_barrier(0);
         mul4(f, hi1, Y, 2);
         mul4(f, lo1, Y, 2);
+        __builtin_amdgcn_sched_barrier(0);
         next();
+        __builtin_amdgcn_sched_barrier(0);
         mul4(f2, hi1, Y, 2);
     } else {
         right(X[2], X[3], s, hi1, lo1);

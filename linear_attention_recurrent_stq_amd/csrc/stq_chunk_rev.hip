@@ -86,22 +86,28 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
     // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
     const int row0 = 4 * g + (c16 & 3);
     const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
-    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
+    const size_t col4 = (size_t)h * (DV / 4) + col0 / 4;
+    const uint32_t lane4 = c16 >> 2;     // (offsets of a lane stay 32 bits, bases in scalar registers)
     half8 f[4], f2[4];
-    int which = 0;
+    // The lane's numbers, formed anew in every step: what depends on them alone would be kept in
+    // registers over the loop.
+    auto anew = [](int x) {
+        asm volatile("" : "+v"(x));
+        return x;
+    };
 
     if (wave >= NW) {                    // what dO gives to 16 columns
         if (nc == 0) return;
         raw v[4];                        // dO of the next chunk
         auto load_v = [&](int c) {
             const raw *base = static_cast<const raw *>(A.dout) + (size_t)(t0 + c * kC) * row_step + col4;
-            const int n = t1 - t0 - c * kC;
+            const int n = t1 - t0 - c * kC, at = anew(row0);
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + row0, n - 1) * row_step];
+            for (int rt = 0; rt < 4; ++rt) v[rt] = base[(uint32_t)min(16 * rt + at, n - 1) * row_step + lane4];
         };
         load_v(nc - 1);
         for (int i = 0; i < nc; ++i) {
-            const int c = nc - 1 - i, n = t1 - t0 - c * kC;
+            const int c = nc - 1 - i, n = t1 - t0 - c * kC, r16 = anew(c16);
             floatx4 D[4], y[4];
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             }
             if (c > 0) load_v(c - 1);
             lds_barrier();
-            const lds_float m = float_at(&sh.m[which], 4 * g);
+            const lds_float m = float_at(&sh.m[i & 1], 4 * g);
             float undo;
             upper<!BF16>(half_at(&sh.P, lane * 8), D, y, undo);
 #pragma unroll
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             for (int ks = 0; ks < 2; ++ks) right(D[2 * ks], D[2 * ks + 1], sd, dh[ks], dl[ks]);
             lds_half vb[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) vb[j] = half_at(&sh.V, place_w(c16, g, j));
+            for (int j = 0; j < 4; ++j) vb[j] = half_at(&sh.V, place_w(r16, g, j));
             auto load_c = [&](half8 (&x)[4], int l, int c0, int ks) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = frag(vb[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
@@ -144,11 +150,11 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             load_c(f, 0, 0, 0);
             columns_times<CT, NQ>(load_c, dh, dl, f, f2, [&](int ct, floatx4 z) { sh.zd[mine][ct][lane] = z * undo; });
             lds_barrier();
-            which = which == 2 ? 0 : which + 1;
         }
         return;
     }
 
+    __builtin_amdgcn_s_setprio(3);       // the chain goes first where waves of a SIMD could both issue
     floatx4 S[CT];
     const size_t state0 = ((size_t)b * H + h) * DK * DV + col0;
     uint32_t at0 = 4 * g * DV + c16;     // of the lane's first value in the state
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
     asm volatile("" : "+v"(at0));
 
     for (int i = 0; i < nc; ++i) {
-        const int c = nc - 1 - i, n = t1 - t0 - c * kC;
+        const int c = nc - 1 - i, n = t1 - t0 - c * kC, r16 = anew(c16), at = anew(row0);
         const size_t entry = entry0 + (size_t)c * H;
         store_tiles(A.dS + entry * (DK * DV) + col0 * DK, S, CT);
         floatx4 R[4], y[4];
@@ -168,8 +174,8 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) R[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
         lds_barrier();
-        const lds_float m = float_at(&sh.m[which], 4 * g);
-        rows_times<KS, NK>([&](int ks) { return half_at(&sh.K, place_k(c16, g, ks)) + ks * kFrag; },
+        const lds_float m = float_at(&sh.m[i & 1], 4 * g);
+        rows_times<KS, NK>([&](int ks) { return half_at(&sh.K, place_k(r16, g, ks)) + ks * kFrag; },
                            [&](int ks, half8 &hi, half8 &lo) { right(S[2 * ks], S[2 * ks + 1], s, hi, lo); }, R, f, f2);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             quad_transpose(z);
             raw out;
             narrow(z, out);
-            if (16 * rt + row0 < n) dv[(uint32_t)(16 * rt + row0) * row_step] = out;
+            if (16 * rt + at < n) dv[(uint32_t)(16 * rt + at) * row_step + lane4] = out;
         }
         store_tiles(A.y + entry * (kC * DV) + col0 * kC, y, 4);
         const float su = scale_to(column_max(R), 13, undo);
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
         for (int ks = 0; ks < 2; ++ks) right(R[2 * ks], R[2 * ks + 1], su, kh[ks], kl[ks]);
         lds_half wb[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wb[j] = half_at(&sh.W, place_w(c16, g, j));
+        for (int j = 0; j < 4; ++j) wb[j] = half_at(&sh.W, place_w(r16, g, j));
         auto load_w = [&](half8 (&x)[4], int l, int c0, int ks) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = frag(wb[j] + ((l * CT + c0 + j) * 2 + ks) * kFrag);
@@ -217,7 +223,6 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[ct][r] = __builtin_fmaf(z[r], undo, __builtin_fmaf(S[ct][r], d[r], q[r]));
         });
-        which = which == 2 ? 0 : which + 1;
     }
     if (!A.dinitial) return;
 #pragma unroll

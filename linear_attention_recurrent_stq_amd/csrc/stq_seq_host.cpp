@@ -39,7 +39,7 @@ stq_status check_rule(const stq_rule *r) {
 
 stq_status check_sizes(const stq_rule *r, int32_t B, int32_t N) {
     if (B < 0 || N < 0) return fail(STQ_ERR_INVALID, "B and N must be >= 0");
-    if ((int64_t)B * r->H * 2 > INT32_MAX) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^30");
+    if ((int64_t)B * r->H * 4 > INT32_MAX) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^29");
     return STQ_OK;
 }
 
@@ -90,6 +90,17 @@ size_t carve(const stq_rule *r, int32_t B, int32_t N, bool backward, void *base,
     a->order = B > 1 && B <= stq::kOrdered ? static_cast<int32_t *>(base) : nullptr;
     a->prep = reinterpret_cast<stq::ChunkPrep *>(take(sizeof(stq::ChunkPrep)));
     if (r->gate == STQ_GATE_KEYVEC) a->gates = reinterpret_cast<stq::ChunkGates *>(take(sizeof(stq::ChunkGates)));
+    const int64_t steps = stq::chunk_steps(r->H, r->d_v, N);
+    if (!backward && steps > 0) {
+        auto more = [&](int64_t n, int cols) {
+            float *p = reinterpret_cast<float *>(static_cast<char *>(base) + at);
+            at += (size_t)n * r->d_k * cols * sizeof(float);
+            return p;
+        };
+        a->steps = more(steps, r->d_v + r->d_k);
+        a->starts = more(2 * steps, r->d_v);
+    }
+    a->segs = backward ? 1 : stq::chunk_segments(r->H, r->d_k, r->d_v, B, N);
     if (backward) {
         a->back = reinterpret_cast<stq::ChunkBack *>(take(sizeof(stq::ChunkBack)));
         a->S = reinterpret_cast<float *>(take(sizeof(float) * r->d_k * r->d_v));

@@ -294,6 +294,45 @@ def test_chunk_forward_sequences_apart(stq):
         assert (guard[at[-1]:] == 7).all()
 
 
+# A long sequence, alone or with few others, passes in segments: a segment's end from no state
+# and its matrix are each within the tolerance of a state passing through it, hence twice that.
+@pytest.mark.parametrize("lens", [[3500], [4000, 2300], [9300, 5, 0]])
+@pytest.mark.parametrize("dk,dv,keyvec,bf16", [(64, 128, False, False), (128, 64, False, True), (64, 64, True, False),
+                                               (128, 128, True, True), (128, 128, False, True)])
+def test_chunk_forward_long(stq, lens, dk, dv, keyvec, bf16):
+    rng = np.random.default_rng(dk + 5 * dv)
+    H = 1
+    at, cu = _cu(lens)
+    n, B = at[-1] + 2, len(lens)
+    x, y = _inputs(rng, n, H, dk, dv, keyvec, bf16, lo=0.998)
+    S0 = rng.normal(size=(B, H, dk, dv)).astype(np.float32)
+    S = torch.from_numpy(S0).cuda()
+    plan = stq.ChunkPlan(H, dk, dv, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32, max_tokens=n + 70,
+                         max_seqs=B + 1)
+    plan.workspace.fill_(255)
+    o, last = torch.full_like(x["v"], 7.0), torch.full_like(S, 7.0)
+    ins = (cu, x["q"], x["k"], x["v"], x["a"], x["beta"])
+    stq.chunk_forward(plan, *ins, o, initial_state=S, final_state=last)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), S0)
+    go = o.double().cpu().numpy()
+    assert (go[at[-1]:] == 7).all()
+    _within(go[:at[-1]], wo[:at[-1]], 2 * _chunk_tol(lens) + _io_step(bf16))
+    for t in range(0, at[-1], 500):      # no part is lost in the whole
+        e = min(t + 500, at[-1])
+        _within(go[t:e], wo[t:e], 2 * _chunk_tol(lens) + _io_step(bf16))
+    for b in range(B):
+        _within(last[b].cpu().numpy(), wl[b], 2 * _chunk_tol(lens))
+        if lens[b] == 0:
+            assert torch.equal(last[b], S[b])
+    # in place and again, the same bits; without states, from zero
+    o2 = torch.zeros_like(o)
+    stq.chunk_forward(plan, *ins, o2, initial_state=S, final_state=S)
+    assert torch.equal(o2[:at[-1]], o[:at[-1]]) and torch.equal(S, last)
+    stq.chunk_forward(plan, *ins, o2)
+    wo, _, _ = seqref.forward(at, *(y[m] for m in ("q", "k", "v", "a", "beta")), np.zeros_like(S0))
+    _within(o2.double().cpu().numpy()[:at[-1]], wo[:at[-1]], 2 * _chunk_tol(lens) + _io_step(bf16))
+
+
 def test_chunk_forward_then_steps(stq):
     """The pieces together: a prompt by chunks, its last tokens one by one from
     the state it left, against the whole sequence at once."""
