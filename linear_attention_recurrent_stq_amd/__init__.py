@@ -13,6 +13,7 @@ tokens of each sequence: ``chunk_forward``, ``chunk_backward``,
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -326,44 +327,59 @@ def calibrate(H, d_k, d_v, *, B, steps, inputs, unit=UNIT_HEAD, gate=GATE_SCALAR
 
 # ------------------------------------------------------------- sequences
 
-def _rule(q, v, a):
-    """stq_rule of packed inputs q [N,H,d_k], v [N,H,d_v], a [N,H] or [N,H,d_k]."""
+@functools.lru_cache(maxsize=None)
+def _rule(H, d_k, d_v, gate, io_dtype):
+    return StqRule(H, d_k, d_v, gate, io_dtype)
+
+
+def _at(t, what, dtype, shape, device):
+    """Address of a contiguous tensor of this type and shape on CUDA device number `device`."""
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, what, dtype, shape, device):
+    return None if t is None else _at(t, what, dtype, shape, device)
+
+
+def _run(device, stream, where, *args):
+    """Calls the library's function `where` with `stream` (None: the device's current
+    one) as its last argument, with `device` the current device."""
     import torch
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k must be [N,H,d_k] and v [N,H,d_v]")
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
-    return StqRule(q.shape[1], q.shape[2], v.shape[2], GATE_KEYVEC if a.dim() == 3 else GATE_SCALAR,
-                   BF16 if q.dtype == torch.bfloat16 else F32)
-
-
-def _one_device(ref, **tensors):
-    """Every given tensor on the device of `ref`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _run(device, stream, where, *args)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    _check(getattr(_lib, where)(*args, s.cuda_stream), where)
 
 
 def _seq_inputs(cu_seqlens, q, k, v, a, beta):
-    """Checks a packed batch and returns (rule, B, N, pointers of cu, q, k, v, a, beta)."""
+    """Checks a packed batch q, k [N,H,d_k], v [N,H,d_v], a [N,H] or [N,H,d_k], beta [N,H],
+    cu_seqlens [B+1] int32; returns (rule, device, B, N, addresses of cu, q, k, v, a, beta)."""
     import torch
-    rule = _rule(q, v, a)
-    N, H, dk = q.shape
-    dv, io = v.shape[2], q.dtype
-    if tuple(k.shape) != (N, H, dk) or tuple(v.shape) != (N, H, dv):
+    device, io = q.get_device(), q.dtype
+    if device < 0:
+        raise ValueError("q must be a device tensor")
+    if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k must be [N,H,d_k] and v [N,H,d_v]")
-    if tuple(a.shape) not in ((N, H), (N, H, dk)) or tuple(beta.shape) != (N, H):
-        raise ValueError("a must be [N,H] or [N,H,d_k], beta [N,H]")
+    if io != torch.bfloat16 and io != torch.float32:
+        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {io}")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [B+1]")
-    _one_device(q, cu_seqlens=cu_seqlens, k=k, v=v, a=a, beta=beta)
-    return rule, cu_seqlens.numel() - 1, N, [
-        _dptr(cu_seqlens, "cu_seqlens", torch.int32), _dptr(q, "q"), _dptr(k, "k", io), _dptr(v, "v", io),
-        _dptr(a, "a", torch.float32), _dptr(beta, "beta", torch.float32)]
-
-
-def _opt(t, what, dtype):
-    return None if t is None else _dptr(t, what, dtype)
+    (N, H, dk), dv, n = q.shape, v.shape[2], cu_seqlens.numel()
+    vec, f32 = a.dim() == 3, torch.float32
+    return (_rule(H, dk, dv, GATE_KEYVEC if vec else GATE_SCALAR, BF16 if io == torch.bfloat16 else F32), device,
+            n - 1, N,
+            (_at(cu_seqlens, "cu_seqlens", torch.int32, (n,), device), _at(q, "q", io, (N, H, dk), device),
+             _at(k, "k", io, (N, H, dk), device), _at(v, "v", io, (N, H, dv), device),
+             _at(a, "a", f32, (N, H, dk) if vec else (N, H), device), _at(beta, "beta", f32, (N, H), device)))
 
 
 def recurrent_step(state, slot_ids, cu_seqlens, q, k, v, a, beta, o, commit=None, stream=None) -> None:
@@ -372,20 +388,12 @@ def recurrent_step(state, slot_ids, cu_seqlens, q, k, v, a, beta, o, commit=None
     None: sequence b uses slot b); o [N,H,d_v] fp32.  commit [B] int32: how many
     leading tokens of each request its state takes in (None: all)."""
     import torch
-    rule, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (rule.H, rule.d_k, rule.d_v):
-        raise ValueError("state must be [slots,H,d_k,d_v]")
-    if tuple(o.shape) != (N, rule.H, rule.d_v):
-        raise ValueError("o must be [N,H,d_v]")
-    for t, what in ((slot_ids, "slot_ids"), (commit, "commit")):
-        if t is not None and tuple(t.shape) != (B,):
-            raise ValueError(f"{what} must be [B]")
-    _one_device(q, state=state, slot_ids=slot_ids, commit=commit, o=o)
-    with torch.cuda.device(q.device):
-        _check(_lib.stq_recurrent_step(
-            C.byref(rule), B, N, *ptrs, _dptr(state, "state", torch.float32), state.shape[0],
-            _opt(slot_ids, "slot_ids", torch.int32), _opt(commit, "commit", torch.int32),
-            _dptr(o, "o", torch.float32), _stream_ptr(stream)), "stq_recurrent_step")
+    rule, device, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
+    H, dk, dv, slots = rule.H, rule.d_k, rule.d_v, state.shape[0] if state.dim() else 0
+    _run(device, stream, "stq_recurrent_step", C.byref(rule), B, N, *ptrs,
+         _at(state, "state", torch.float32, (slots, H, dk, dv), device), slots,
+         _opt(slot_ids, "slot_ids", torch.int32, (B,), device), _opt(commit, "commit", torch.int32, (B,), device),
+         _at(o, "o", torch.float32, (N, H, dv), device))
 
 
 class ChunkPlan:
@@ -396,7 +404,7 @@ class ChunkPlan:
     def __init__(self, H, d_k, d_v, *, gate=GATE_SCALAR, io_dtype=BF16, max_tokens, max_seqs,
                  backward=False, device="cuda"):
         import torch
-        self.rule = StqRule(H, d_k, d_v, gate, io_dtype)
+        self.rule = _rule(H, d_k, d_v, gate, io_dtype)
         self.max_tokens, self.max_seqs, self.backward = max_tokens, max_seqs, bool(backward)
         n = C.c_size_t()
         _check(_lib.stq_chunk_workspace(C.byref(self.rule), max_seqs, max_tokens, int(self.backward), C.byref(n)),
@@ -404,24 +412,21 @@ class ChunkPlan:
         self.workspace = torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
 
     def inputs(self, cu_seqlens, q, k, v, a, beta):
-        """Checks a packed batch against the plan; returns (B, N, pointers)."""
-        rule, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
-        if bytes(rule) != bytes(self.rule):
+        """Checks a packed batch against the plan; returns (device, B, N, addresses)."""
+        rule, device, B, N, ptrs = _seq_inputs(cu_seqlens, q, k, v, a, beta)
+        if rule is not self.rule:
             raise ValueError("the batch's heads, sizes, gate or types are not the plan's")
         if B > self.max_seqs or N > self.max_tokens:
             raise ValueError("the batch exceeds the plan")
-        _one_device(q, workspace=self.workspace)
-        return B, N, ptrs
+        if self.workspace.get_device() != device:
+            raise ValueError(f"the plan's workspace is on {self.workspace.device}, the batch on cuda:{device}")
+        return device, B, N, ptrs
 
-    def states(self, B, ref, **states):
-        """Pointers of states [B,H,d_k,d_v] fp32 (None stays None)."""
+    def states(self, B, device, **states):
+        """Addresses of states [B,H,d_k,d_v] fp32 (None stays None)."""
         import torch
-        r = self.rule
-        for name, t in states.items():
-            if t is not None and tuple(t.shape) != (B, r.H, r.d_k, r.d_v):
-                raise ValueError(f"{name} must be [B,H,d_k,d_v]")
-        _one_device(ref, **states)
-        return [_opt(t, name, torch.float32) for name, t in states.items()]
+        shape = (B, self.rule.H, self.rule.d_k, self.rule.d_v)
+        return [_opt(t, name, torch.float32, shape, device) for name, t in states.items()]
 
 
 def chunk_forward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, o, *, initial_state=None,
@@ -429,17 +434,10 @@ def chunk_forward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, o, *, initial_s
     """stq_chunk_forward on torch device tensors: packed q, k [N,H,d_k],
     v [N,H,d_v], a [N,H] or [N,H,d_k], beta [N,H], cu_seqlens [B+1] int32; o
     [N,H,d_v] as v; states [B,H,d_k,d_v] fp32 (final_state may be initial_state)."""
-    import torch
-    B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
-    if o.shape != v.shape:
-        raise ValueError("o must be [N,H,d_v]")
-    first, last = plan.states(B, q, initial_state=initial_state, final_state=final_state)
-    _one_device(q, o=o)
-    with torch.cuda.device(q.device):
-        _check(_lib.stq_chunk_forward(
-            C.byref(plan.rule), B, N, *ptrs, first, _dptr(o, "o", v.dtype), last,
-            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
-            "stq_chunk_forward")
+    device, B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
+    first, last = plan.states(B, device, initial_state=initial_state, final_state=final_state)
+    _run(device, stream, "stq_chunk_forward", C.byref(plan.rule), B, N, *ptrs, first,
+         _at(o, "o", v.dtype, v.shape, device), last, plan.workspace.data_ptr(), plan.workspace.numel())
 
 
 def chunk_backward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, do, dq, dk, dv, da, dbeta, *,
@@ -447,24 +445,16 @@ def chunk_backward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, do, dq, dk, dv
     """stq_chunk_backward on torch device tensors: from the gradients do [N,H,d_v]
     (as v) and d_final_state of chunk_forward's outputs, those of its inputs, each of its
     input's shape and type.  The plan needs backward=True."""
-    import torch
     if not plan.backward:
         raise ValueError("the plan has no room for the backward pass (backward=True)")
-    B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
-    outs = []
-    for t, like, what in ((do, v, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (da, a, "da"),
-                          (dbeta, beta, "dbeta")):
-        if t.shape != like.shape:
-            raise ValueError(f"{what} must be {tuple(like.shape)}")
-        outs.append(_dptr(t, what, like.dtype))
-    _one_device(q, do=do, dq=dq, dk=dk, dv=dv, da=da, dbeta=dbeta)
-    first, dlast, dfirst = plan.states(B, q, initial_state=initial_state, d_final_state=d_final_state,
+    device, B, N, ptrs = plan.inputs(cu_seqlens, q, k, v, a, beta)
+    outs = [_at(t, what, like.dtype, like.shape, device)
+            for t, like, what in ((do, v, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (da, a, "da"),
+                                  (dbeta, beta, "dbeta"))]
+    first, dlast, dfirst = plan.states(B, device, initial_state=initial_state, d_final_state=d_final_state,
                                        d_initial_state=d_initial_state)
-    with torch.cuda.device(q.device):
-        _check(_lib.stq_chunk_backward(
-            C.byref(plan.rule), B, N, *ptrs, first, outs[0], dlast, *outs[1:], dfirst,
-            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
-            "stq_chunk_backward")
+    _run(device, stream, "stq_chunk_backward", C.byref(plan.rule), B, N, *ptrs, first, outs[0], dlast, *outs[1:],
+         dfirst, plan.workspace.data_ptr(), plan.workspace.numel())
 
 
 class VerifyPlan:
@@ -487,26 +477,20 @@ def verify_draft(plan: VerifyPlan, draft_tokens, target, draft, uniform, n_accep
     [B] int32 or None; writes n_accepted and next_token [B] int32.  With T = 0
     (draft_tokens and draft of no elements) next_token is drawn from target."""
     import torch
-    io = torch.bfloat16 if plan.dtype == BF16 else torch.float32
+    io, i32 = torch.bfloat16 if plan.dtype == BF16 else torch.float32, torch.int32
     if draft_tokens.dim() != 2:
         raise ValueError("draft_tokens must be [B,T]")
-    B, T = draft_tokens.shape
+    device = target.get_device()
+    if device < 0:
+        raise ValueError("target must be a device tensor")
+    (B, T), V = draft_tokens.shape, plan.V
     if B > plan.max_requests or T > plan.max_draft:
         raise ValueError("the batch exceeds the plan")
-    if (tuple(target.shape) != (B, T + 1, plan.V) or tuple(draft.shape) != (B, T, plan.V)
-            or tuple(uniform.shape) != (B, T + 1)):
-        raise ValueError("target must be [B,T+1,V], draft [B,T,V], uniform [B,T+1]")
-    for t, what in ((n_accepted, "n_accepted"), (next_token, "next_token"), (draft_len, "draft_len")):
-        if t is not None and tuple(t.shape) != (B,):
-            raise ValueError(f"{what} must be [B]")
-    _one_device(target, draft_tokens=draft_tokens, draft=draft, uniform=uniform, n_accepted=n_accepted,
-                next_token=next_token, draft_len=draft_len, workspace=plan.workspace)
-    i32 = torch.int32
-    with torch.cuda.device(target.device):
-        _check(_lib.stq_verify_draft(
-            B, T, plan.V, plan.dtype, _dptr(draft_tokens, "draft_tokens", i32) if T else None,
-            _opt(draft_len, "draft_len", i32), _dptr(target, "target", io),
-            _dptr(draft, "draft", io) if T else None, _dptr(uniform, "uniform", torch.float32),
-            _dptr(n_accepted, "n_accepted", i32), _dptr(next_token, "next_token", i32),
-            C.c_void_p(plan.workspace.data_ptr()), plan.workspace.numel(), _stream_ptr(stream)),
-            "stq_verify_draft")
+    if plan.workspace.get_device() != device:
+        raise ValueError(f"the plan's workspace is on {plan.workspace.device}, target on cuda:{device}")
+    tokens, q = _at(draft_tokens, "draft_tokens", i32, (B, T), device), _at(draft, "draft", io, (B, T, V), device)
+    _run(device, stream, "stq_verify_draft", B, T, V, plan.dtype, tokens if T else None,
+         _opt(draft_len, "draft_len", i32, (B,), device), _at(target, "target", io, (B, T + 1, V), device),
+         q if T else None, _at(uniform, "uniform", torch.float32, (B, T + 1), device),
+         _at(n_accepted, "n_accepted", i32, (B,), device), _at(next_token, "next_token", i32, (B,), device),
+         plan.workspace.data_ptr(), plan.workspace.numel())
