@@ -312,8 +312,9 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
  *   d_o       [N,H,d_v] io_dtype
  * States and sums are fp32; products take fp32 operands as scaled fp16 pairs
  * (22 bits), so results are those of fp32 arithmetic to a few ulp of their
- * row's and column's norm.  Results do not depend on the batch around a
- * sequence's place in its chunks of 64, and are the same at every run.
+ * row's and column's norm, and the same at every run.  Few long sequences are
+ * passed through in segments (by a rule on B, N, H, d_k and d_v), joined by fp32
+ * products; calls that differ there may differ in the last bits.
  * Allocates nothing, does not synchronize, may be captured in a HIP graph.  A
  * workspace must not be used by two calls that overlap in time.
  * Errors: STQ_ERR_INVALID (NULL, B or N negative, a bad rule),

@@ -440,6 +440,29 @@ def chunk_forward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, o, *, initial_s
          _at(o, "o", v.dtype, v.shape, device), last, plan.workspace.data_ptr(), plan.workspace.numel())
 
 
+def prefill(pool: Pool, plan: ChunkPlan, slot_ids, cu_seqlens, q, k, v, a, beta, o, states, *, resume=False,
+            stream=None) -> None:
+    """A prompt of each request, or its next part, into the request's slot, so that
+    decode_step goes on from it: chunk_forward, then pack (with resume, unpack first: the
+    slots' states are where the parts begin; else they begin at zero).  slot_ids [B]
+    int32, distinct; states [B,H,d_k,d_v] fp32, which holds the last states afterwards."""
+    import torch
+    L = pool.layout
+    if plan.rule is not _rule(L.H, L.d_k, L.d_v, L.gate, L.io_dtype):
+        raise ValueError("the plan's heads, sizes, gate or types are not the pool's")
+    device, B, _, _ = plan.inputs(cu_seqlens, q, k, v, a, beta)
+    if states is None or pool.buffer.get_device() != device:
+        raise ValueError(f"states must be given and the pool be on cuda:{device}")
+    _at(slot_ids, "slot_ids", torch.int32, (B,), device)
+    plan.states(B, device, states=states)
+    with torch.cuda.device(device):
+        if resume:
+            unpack(pool, slot_ids, states, stream)
+        chunk_forward(plan, cu_seqlens, q, k, v, a, beta, o, initial_state=states if resume else None,
+                      final_state=states, stream=stream)
+        pack(pool, slot_ids, states, stream)
+
+
 def chunk_backward(plan: ChunkPlan, cu_seqlens, q, k, v, a, beta, do, dq, dk, dv, da, dbeta, *,
                    initial_state=None, d_final_state=None, d_initial_state=None, stream=None) -> None:
     """stq_chunk_backward on torch device tensors: from the gradients do [N,H,d_v]

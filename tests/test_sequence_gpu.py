@@ -358,6 +358,84 @@ def test_chunk_forward_then_steps(stq):
     _within(o1.double().cpu().numpy().reshape(B, cut, H, d), wo[:, :cut], tol + 2.0 ** -8)
 
 
+@pytest.mark.parametrize("kw", [{}, {"window": 4}, {"scale_fit": 1}])
+def test_serving(stq, kw):
+    """A request's whole life: its prompt in two parts into a pool of fp32 and 8-bit units, decode
+    steps from there; drafted tokens run ahead on the fp32 states, checked, and committed."""
+    rng = np.random.default_rng(21)
+    H, d, B, slots = 4, 128, 3, 5
+    lens, tail = [130, 1, 77], 4
+    at, cu = _cu(lens)
+    n = at[-1]
+    x, y = _inputs(rng, n, H, d, d, True, True)
+    names = ("q", "k", "v", "a", "beta")
+    bits = np.full(H, 8, np.uint8) if kw else np.array([32, 32, 8, 32], np.uint8)
+    L = stq.Layout(H, d, d, bits, gate=stq.GATE_KEYVEC, **kw)
+    pool, plan = stq.Pool(L, slots), stq.ChunkPlan(H, d, d, gate=1, max_tokens=n, max_seqs=B)
+    ids = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    states, o = torch.empty(B, H, d, d, device="cuda"), torch.empty_like(x["v"])
+    stq.prefill(pool, plan, ids, cu, *[x[m] for m in names], o, states)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in names), np.zeros((B, H, d, d)))
+    _within(o.double().cpu().numpy(), wo, _chunk_tol(lens) + 2.0 ** -8)
+    _within(states.cpu().numpy(), wl, _chunk_tol(lens))
+    # the pool holds what packing these states gives, and the next part begins from it
+    held, other = torch.empty_like(states), stq.Pool(L, slots)
+    stq.unpack(pool, ids, held)
+    stq.pack(other, ids, states)
+    again = torch.empty_like(states)
+    stq.unpack(other, ids, again)
+    assert torch.equal(held, again)
+    x2, y2 = _inputs(rng, n, H, d, d, True, True)
+    stq.prefill(pool, plan, ids, cu, *[x2[m] for m in names], o, states, resume=True)
+    wo, wl, _ = seqref.forward(at, *(y2[m] for m in names), held.double().cpu().numpy())
+    _within(o.double().cpu().numpy(), wo, _chunk_tol(lens) + 2.0 ** -8)
+    _within(states.cpu().numpy(), wl, _chunk_tol(lens))
+    # decode steps on the pool: the same as on the unpacked state while the units are fp32
+    stq.unpack(pool, ids, held)
+    x3, y3 = _inputs(rng, B, H, d, d, True, True)
+    od = torch.empty(B, H, d, device="cuda")
+    stq.decode_step(pool, ids, *[x3[m] for m in names], od)
+    wo, _, _ = seqref.forward(list(range(B + 1)), *(y3[m] for m in names), held.double().cpu().numpy())
+    if not kw:
+        _within(od.cpu().numpy()[:, [0, 1, 3]], wo[:, [0, 1, 3]], _step_tol(d, 1))
+    # drafted tokens: ahead of the states, accepted or not, then taken in
+    T, V = tail, 37
+    xd, yd = _inputs(rng, B * T, H, d, d, True, True)
+    cud, S = _cu([T] * B)[1], states.clone()
+    od = torch.empty(B * T, H, d, device="cuda")
+    p = rng.random((B, T + 1, V)).astype(np.float32)
+    q = rng.random((B, T, V)).astype(np.float32)
+    p, q = p / p.sum(-1, keepdims=True), q / q.sum(-1, keepdims=True)
+    tok, r = rng.integers(0, V, (B, T)).astype(np.int32), rng.random((B, T + 1)).astype(np.float32)
+    acc, nxt = (torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    check = stq.VerifyPlan(B, T, V)
+    stq.recurrent_step(S, None, cud, *[xd[m] for m in names], od, commit=torch.zeros_like(acc))
+    assert torch.equal(S, states)
+    stq.verify_draft(check, _dev(tok, torch.int32), *[_dev(z, torch.float32) for z in (p, q, r)], acc, nxt)
+    wa, _ = seqref.verify(tok, None, p, q, r)
+    assert (acc.cpu().numpy() == wa).all()
+    stq.recurrent_step(S, None, cud, *[xd[m] for m in names], od, commit=acc)
+    _, _, kept = seqref.forward(np.arange(B + 1) * T, *(yd[m] for m in names), states.double().cpu().numpy(), wa)
+    _within(S.cpu().numpy(), kept, _step_tol(d, T))
+
+
+def test_prefill_refusals(stq):
+    H, d, n = 2, 64, 5
+    x, _ = _inputs(np.random.default_rng(0), n, H, d, d, False, True)
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    pool = stq.Pool(stq.Layout(H, d, d, np.full(H, 8, np.uint8)), 2)
+    plan = stq.ChunkPlan(H, d, d, max_tokens=n, max_seqs=2)
+    S = torch.zeros(2, H, d, d, device="cuda")
+    good = dict(pool=pool, plan=plan, slot_ids=ids, cu_seqlens=cu, o=torch.empty_like(x["v"]), states=S, **x)
+    for bad in (dict(slot_ids=ids[:1]), dict(states=S[:1]), dict(states=None), dict(states=S.double()),
+                dict(slot_ids=ids.long()), dict(plan=stq.ChunkPlan(H, d, d, gate=1, max_tokens=n, max_seqs=2)),
+                dict(pool=stq.Pool(stq.Layout(H, d, 128, np.full(H, 8, np.uint8)), 2)), dict(o=good["o"][:2])):
+        with pytest.raises((ValueError, stq.StqError)):
+            stq.prefill(**{**good, **bad})
+    stq.prefill(**good)
+
+
 def test_chunk_forward_in_a_graph(stq):
     """Captured once, replayed on new inputs in place, with eager work between."""
     rng = np.random.default_rng(4)

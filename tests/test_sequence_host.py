@@ -83,6 +83,90 @@ def test_verify_workspace(stq):
     assert _verify(stq, B=0) == stq.STQ_OK
 
 
+def _forward(stq, rule, **kw):
+    x = dict(B=2, N=200, cu=P, q=P, k=P, v=P, a=P, beta=P, first=P, o=P, last=P, ws=P, n=1 << 40)
+    x.update(kw)
+    return stq.library().stq_chunk_forward(
+        None if rule is None else C.byref(rule), x["B"], x["N"], x["cu"], x["q"], x["k"], x["v"], x["a"], x["beta"],
+        x["first"], x["o"], x["last"], x["ws"], x["n"], None)
+
+
+def _backward(stq, rule, **kw):
+    x = dict(B=2, N=200, cu=P, q=P, k=P, v=P, a=P, beta=P, first=P, do=P, dlast=P, dq=P, dk=P, dv=P, da=P, dbeta=P,
+             dfirst=P, ws=P, n=1 << 40)
+    x.update(kw)
+    return stq.library().stq_chunk_backward(
+        None if rule is None else C.byref(rule), x["B"], x["N"], x["cu"], x["q"], x["k"], x["v"], x["a"], x["beta"],
+        x["first"], x["do"], x["dlast"], x["dq"], x["dk"], x["dv"], x["da"], x["dbeta"], x["dfirst"], x["ws"], x["n"],
+        None)
+
+
+def _workspace(stq, rule, B, N, backward):
+    n = C.c_size_t()
+    return stq.library().stq_chunk_workspace(C.byref(rule), B, N, backward, C.byref(n)), n.value
+
+
+@pytest.mark.parametrize("bad,status", RULES)
+def test_chunk_refuses_a_rule(stq, bad, status):
+    for call in (_forward, _backward):
+        assert call(stq, _rule(stq, **bad)) == status
+        assert stq.library().stq_last_error().decode()
+        assert call(stq, None) == 1
+    assert _workspace(stq, _rule(stq, **bad), 1, 1, 0)[0] == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"B": -1}, 1), ({"N": -1}, 1), ({"cu": None}, 1), ({"q": None}, 1), ({"k": None}, 1), ({"v": None}, 1),
+    ({"a": None}, 1), ({"beta": None}, 1), ({"ws": None}, 1), ({"ws": P + 8}, 4), ({"q": P + 8}, 4), ({"k": P + 4}, 4),
+    ({"beta": P + 4}, 4), ({"cu": P + 2}, 4), ({"first": P + 8}, 4), ({"n": 1000}, 3), ({"B": 1 << 29}, 2),
+    ({"B": 1 << 20, "N": (1 << 31) - 1}, 2)])
+def test_chunk_refuses_arguments(stq, kw, status):
+    many = _rule(stq, H=128)             # heads enough for the last two
+    for call in (_forward, _backward):
+        assert call(stq, many, **kw) == status
+        assert stq.library().stq_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,status", [({"o": None}, 1), ({"o": P + 2}, 4), ({"last": P + 4}, 4)])
+def test_chunk_forward_refuses_outputs(stq, kw, status):
+    assert _forward(stq, _rule(stq), **kw) == status
+
+
+@pytest.mark.parametrize("name", ["do", "dq", "dk", "dv", "da", "dbeta"])
+def test_chunk_backward_refuses_outputs(stq, name):
+    assert _backward(stq, _rule(stq), **{name: None}) == 1
+    assert _backward(stq, _rule(stq), **{name: P + 8}) == 4
+    for states in ("dlast", "dfirst"):
+        assert _backward(stq, _rule(stq), **{states: P + 4}) == 4
+
+
+def test_chunk_nothing_to_do(stq):
+    assert _forward(stq, _rule(stq), B=0, cu=None, ws=None) == stq.STQ_OK
+    assert _backward(stq, _rule(stq), B=0, cu=None, ws=None) == stq.STQ_OK
+
+
+@pytest.mark.parametrize("gate", [0, 1])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_chunk_workspace(stq, gate, backward):
+    """Grows with both numbers, so a plan holds every smaller batch; the size that it names is the
+    one that a call asks for."""
+    rule = _rule(stq, gate=gate, H=3)
+    last = 0
+    for N in (0, 1, 64, 1000, 1024, 2047, 2048, 5000, 20000, 100000):
+        for B in (1, 2, 7, 1000, 2000):
+            s, n = _workspace(stq, rule, B, N, backward)
+            assert s == 0
+            assert n >= _workspace(stq, rule, max(1, B // 2), N, backward)[1]
+            assert n >= _workspace(stq, rule, B, N // 2, backward)[1]
+            assert n >= _workspace(stq, rule, B, max(0, N - 1), backward)[1]
+        assert n >= last
+        last = n
+    call = _backward if backward else _forward
+    assert call(stq, rule, n=_workspace(stq, rule, 2, 200, backward)[1] - 1) == 3
+    assert stq.library().stq_chunk_workspace(C.byref(rule), 1, 1, backward, None) == 1
+    assert _workspace(stq, rule, -1, 1, backward)[0] == 1 and _workspace(stq, rule, 1, -1, backward)[0] == 1
+
+
 def test_reference_gradients_against_differences():
     rng = np.random.default_rng(0)
     for keyvec in (False, True):
