@@ -181,6 +181,14 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
     const bool on = own < n;
     const size_t tok = (size_t)(first + min(own, n - 1)) * s.H + h;
 
+    // the states' tiles on their way before they are wanted: the gradient's while the first one is
+    // multiplied
+    floatx4 S[DV / 16], dS[DV / 16];
+    auto fetch = [&](const float *states, floatx4 (&x)[DV / 16]) {
+        const int ct = min(wave_index(), CT - 1);
+#pragma unroll
+        for (int cb = 0; cb < DV / 16; ++cb) x[cb] = four(states + entry * (DK * DV) + (cb * CT + ct) * 256 + 4 * untwist());
+    };
     // ---- own rows of dO, y and w as right operands
     half8 oh[DVS], ol[NO == 2 ? DVS : 1], yh[DVS], yl[DVS], wh[DVS], wl[DVS];
     float own_io, own_iy, own_iw;
@@ -200,6 +208,7 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
                 mx = fmaxf(mx, fabsf(a[e]));
             }
         }
+        fetch(A.S, S);
         sc = scale_to(max_groups(mx), 13, own_iy);
 #pragma unroll
         for (int i = 0; i < DVS; ++i) split8(x[i], sc, yh[i], yl[i]);
@@ -232,21 +241,6 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
             if constexpr (NO == 2) ol[i] = lo;
         }
     }
-    if (half == 0) {
-#pragma unroll
-        for (int i = 0; i < DVS; ++i) {
-            sh.t.w[0][w][i][lane] = wh[i];
-            sh.t.w[1][w][i][lane] = wl[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < DVS; ++i) {
-            sh.t.y[0][w][i][lane] = yh[i];
-            sh.t.y[1][w][i][lane] = yl[i];
-            sh.t.o[0][w][i][lane] = oh[i];
-            if constexpr (NO == 2) sh.t.o[NO - 1][w][i][lane] = ol[i];
-        }
-    }
     const float own_be = m.be[own], sk = m.sk[own], sq = m.sq[own];
     const float own_ik = 1.f / sk, own_iq = 1.f / sq;  // (powers of two)
     if (half == 0 && g == 0) {
@@ -277,6 +271,101 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
             sh.pre[lane] = p;
             sh.suf[lane] = f;
             sh.ga[lane] = a;
+        }
+    }
+
+    // ---- the states' parts: S dO, S y, dS w over the wave's half of the channels
+    floatx4 vq[T], vk[T], vw[T];
+    // a wave turns 16 channels of a state (tile), as they come (raw), into left operands
+    const int tile = wave_index();
+    auto put = [&](const floatx4 (&raw)[DV / 16], const floatx4 *dot_with) {
+        if (tile < CT) {
+            float x[DV / 16][4], mx = 0.f, inv;
+            floatx4 dot = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int cb = 0; cb < DV / 16; ++cb) {
+                if (dot_with) dot += raw[cb] * dot_with[cb];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[cb][r] = raw[cb][r];
+                quad_transpose(x[cb]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(x[cb][r]));
+            }
+            const float sc = scale_to(max_groups(mx), 10, inv);
+#pragma unroll
+            for (int cb = 0; cb < DV / 16; ++cb) {
+                half4 hi, lo;
+                split4(floatx4{x[cb][0], x[cb][1], x[cb][2], x[cb][3]}, sc, hi, lo);
+                const int at = place(c16, g, cb >> 1);
+                reinterpret_cast<half4 *>(&sh.st[0][tile][cb >> 1][at])[cb & 1] = hi;
+                reinterpret_cast<half4 *>(&sh.st[1][tile][cb >> 1][at])[cb & 1] = lo;
+            }
+            if (g == 0) sh.srow[16 * tile + c16] = inv;
+            if (dot_with) {              // before the turn a lane has a column of channels 4 (c16 / 4) ..
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float d = dot[r];
+                    d += dpp0<quad(1, 0, 3, 2)>(d);
+                    d += dpp0<quad(2, 3, 0, 1)>(d);
+                    dot[r] = sum_groups(d);
+                }
+                if (g == 0 && (c16 & 3) == 0) *reinterpret_cast<floatx4 *>(&sh.rho[16 * tile + c16]) = dot;
+            }
+        }
+        __syncthreads();
+    };
+    put(S, nullptr);
+    fetch(A.dS, dS);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int ct = half * T + t;
+        vq[t] = vk[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < DVS; ++i) {
+            const int at = place(c16, g, i);
+            const half8 lh = sh.st[0][ct][i][at], ll = sh.st[1][ct][i][at];
+            vq[t] = mul<true, NO == 2>(lh, ll, oh[i], ol[NO == 2 ? i : 0], vq[t]);
+            vk[t] = mul<true, true>(lh, ll, yh[i], yl[i], vk[t]);
+        }
+        const floatx4 f = four(&sh.srow[16 * ct + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            vq[t][r] = (vq[t][r] * f[r]) * own_io;
+            vk[t][r] = -((vk[t][r] * f[r]) * own_iy) * own_be;
+        }
+    }
+    __syncthreads();
+    put(dS, S);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int ct = half * T + t;
+        vw[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < DVS; ++i) {
+            const int at = place(c16, g, i);
+            vw[t] = mul<true, true>(sh.st[0][ct][i][at], sh.st[1][ct][i][at], wh[i], wl[i], vw[t]);
+        }
+        const floatx4 f = four(&sh.srow[16 * ct + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vw[t][r] = ((vw[t][r] * f[r]) * own_iw) * own_be;
+    }
+    __syncthreads();
+
+
+    if (half == 0) {
+#pragma unroll
+        for (int i = 0; i < DVS; ++i) {
+            sh.t.w[0][w][i][lane] = wh[i];
+            sh.t.w[1][w][i][lane] = wl[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < DVS; ++i) {
+            sh.t.y[0][w][i][lane] = yh[i];
+            sh.t.y[1][w][i][lane] = yl[i];
+            sh.t.o[0][w][i][lane] = oh[i];
+            if constexpr (NO == 2) sh.t.o[NO - 1][w][i][lane] = ol[i];
         }
     }
     __syncthreads();
@@ -359,81 +448,6 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
                 }
     }
 
-    // ---- the states' parts: S dO, S y, dS w over the wave's half of the channels
-    floatx4 vq[T], vk[T], vw[T];
-    auto stage = [&](const float *from, const float *dot_with) {
-        __syncthreads();
-        const int ct = wave_index();
-        if (ct < CT) {                   // a wave turns 16 channels
-            float x[DV / 16][4], mx = 0.f, inv;
-            floatx4 dot = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int cb = 0; cb < DV / 16; ++cb) {
-                const floatx4 v = four(from + (cb * CT + ct) * 256 + 4 * untwist());
-                if (dot_with) dot += v * four(dot_with + (cb * CT + ct) * 256 + 4 * untwist());
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[cb][r] = v[r];
-                quad_transpose(x[cb]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(x[cb][r]));
-            }
-            const float sc = scale_to(max_groups(mx), 10, inv);
-#pragma unroll
-            for (int cb = 0; cb < DV / 16; ++cb) {
-                half4 hi, lo;
-                split4(floatx4{x[cb][0], x[cb][1], x[cb][2], x[cb][3]}, sc, hi, lo);
-                const int at = place(c16, g, cb >> 1);
-                reinterpret_cast<half4 *>(&sh.st[0][ct][cb >> 1][at])[cb & 1] = hi;
-                reinterpret_cast<half4 *>(&sh.st[1][ct][cb >> 1][at])[cb & 1] = lo;
-            }
-            if (g == 0) sh.srow[16 * ct + c16] = inv;
-            if (dot_with) {              // before the turn a lane has a column of channels 4 (c16 / 4) ..
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float d = dot[r];
-                    d += dpp0<quad(1, 0, 3, 2)>(d);
-                    d += dpp0<quad(2, 3, 0, 1)>(d);
-                    dot[r] = sum_groups(d);
-                }
-                if (g == 0 && (c16 & 3) == 0) *reinterpret_cast<floatx4 *>(&sh.rho[16 * ct + c16]) = dot;
-            }
-        }
-        __syncthreads();
-    };
-    const float *S = A.S + entry * (DK * DV), *dS = A.dS + entry * (DK * DV);
-    stage(S, nullptr);
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        const int ct = half * T + t;
-        vq[t] = vk[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < DVS; ++i) {
-            const int at = place(c16, g, i);
-            const half8 lh = sh.st[0][ct][i][at], ll = sh.st[1][ct][i][at];
-            vq[t] = mul<true, NO == 2>(lh, ll, oh[i], ol[NO == 2 ? i : 0], vq[t]);
-            vk[t] = mul<true, true>(lh, ll, yh[i], yl[i], vk[t]);
-        }
-        const floatx4 f = four(&sh.srow[16 * ct + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            vq[t][r] = (vq[t][r] * f[r]) * own_io;
-            vk[t][r] = -((vk[t][r] * f[r]) * own_iy) * own_be;
-        }
-    }
-    stage(dS, S);
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        const int ct = half * T + t;
-        vw[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < DVS; ++i) {
-            const int at = place(c16, g, i);
-            vw[t] = mul<true, true>(sh.st[0][ct][i][at], sh.st[1][ct][i][at], wh[i], wl[i], vw[t]);
-        }
-        const floatx4 f = four(&sh.srow[16 * ct + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vw[t][r] = ((vw[t][r] * f[r]) * own_iw) * own_be;
-    }
     __syncthreads();
 
     // ---- own rows of k and q with tokens in the lanes: channels 16 ct + 4 g .. + 3 of tile ct
