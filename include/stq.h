@@ -262,7 +262,7 @@ stq_status stq_allocate_bits(int32_t n_units, const float *gate_mean, const floa
  *   d_beta   [N,H] fp32 write strengths
  * Tokens outside every sequence are not read, and their outputs keep what
  * they held.  Inputs are finite; a NaN or infinity reaches only the outputs of its own
- * sequence and head.  States are [.,H,d_k,d_v] fp32, key-row-major, as
+ * sequence and head.  Outputs overlap no input unless a call says so.  States are [.,H,d_k,d_v] fp32, key-row-major, as
  * stq_pack and stq_unpack take them.
  * Per token: S' = diag(a) S, u = beta (v - S'^T k), S = S' + k u^T, o = S^T q.
  */
@@ -289,7 +289,8 @@ typedef struct {
  * right too, and faster with stq_chunk_forward.  Allocates nothing, does not
  * synchronize, may be captured in a HIP graph.
  * Errors: STQ_ERR_INVALID (NULL, B or N negative, B > slots, a bad rule),
- * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128), STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, B * H over 2^20), STQ_ERR_ALIGN,
+ * STQ_ERR_DEVICE.
  */
 stq_status stq_recurrent_step(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
                               const void *d_q, const void *d_k, const void *d_v, const float *d_a,
@@ -318,8 +319,8 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
  * Allocates nothing, does not synchronize, may be captured in a HIP graph.  A
  * workspace must not be used by two calls that overlap in time.
  * Errors: STQ_ERR_INVALID (NULL, B or N negative, a bad rule),
- * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, more than 2^31 chunks times
- * heads), STQ_ERR_TOO_SMALL, STQ_ERR_ALIGN, STQ_ERR_DEVICE.
+ * STQ_ERR_UNSUPPORTED (d_k or d_v not 64/128, B * H over 2^20, (N / 64 + B) * H
+ * over 2^23), STQ_ERR_TOO_SMALL, STQ_ERR_ALIGN, STQ_ERR_DEVICE.
  */
 stq_status stq_chunk_forward(const stq_rule *rule, int32_t B, int32_t N, const int32_t *d_cu_seqlens,
                              const void *d_q, const void *d_k, const void *d_v, const float *d_a,

@@ -134,7 +134,8 @@ __device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(threa
 // lie H d elements apart, often a multiple of the L2's channel interleave, so a head stays in
 // one or two channels: with heads dealt out in turn an XCD would only see heads, and
 // channels, a multiple of 8 apart.  Here it takes m / 8 neighbouring heads of every
-// group, other ones in the next group.
+// group, other ones in the next group.  (Chunk preparation: 240 -> 234 us with scalar, 825 -> 788 us
+// with key-vector gates when it came; the passes neither gain nor lose.)
 __device__ inline void xcd_place(uint32_t id, uint32_t m, uint32_t &group, uint32_t &at) {
     if (m & 7) {
         group = id / m;

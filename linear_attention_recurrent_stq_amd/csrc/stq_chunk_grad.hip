@@ -27,7 +27,6 @@
 //
 // A workgroup holds about 110 KB of LDS and eight waves; the bound is the reading of S, dS, w and
 // y (200 KB a chunk at 128 x 128) and, with key-vector gates, the vector code.
-#include <type_traits>
 
 #include "stq_chunk.h"
 

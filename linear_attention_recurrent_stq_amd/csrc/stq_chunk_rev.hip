@@ -9,7 +9,6 @@
 // Laid out as the pass of the state (stq_chunk_fwd.hip).  The chain from one dS to the next is du,
 // y, dS; the helping waves form what does not depend on it, P^T dO and (Q G)^T dO, and hand it
 // over as result tiles in LDS.
-#include <type_traits>
 
 #include "stq_chunk_pass.h"
 

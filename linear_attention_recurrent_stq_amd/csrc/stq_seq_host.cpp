@@ -37,9 +37,11 @@ stq_status check_rule(const stq_rule *r) {
     return STQ_OK;
 }
 
+// A launch's threads must stay under 2^32: a sequence and head take up to four workgroups of 768 threads,
+// a chunk and head up to 512 (in stq_chunk_workspace).
 stq_status check_sizes(const stq_rule *r, int32_t B, int32_t N) {
     if (B < 0 || N < 0) return fail(STQ_ERR_INVALID, "B and N must be >= 0");
-    if ((int64_t)B * r->H * 4 > INT32_MAX) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^29");
+    if ((int64_t)B * r->H > 1 << 20) return fail(STQ_ERR_UNSUPPORTED, "B * H exceeds 2^20");
     return STQ_OK;
 }
 
@@ -160,8 +162,8 @@ stq_status stq_chunk_workspace(const stq_rule *rule, int32_t B, int32_t N, int32
     if (stq_status s = check_rule(rule)) return s;
     if (stq_status s = check_sizes(rule, B, N)) return s;
     if (!bytes) return fail(STQ_ERR_INVALID, "bytes is NULL");
-    if (((int64_t)N / stq::kC + B) * rule->H >= INT32_MAX)
-        return fail(STQ_ERR_UNSUPPORTED, "too many chunks for one call");
+    if (((int64_t)N / stq::kC + B) * rule->H >= 1 << 23)
+        return fail(STQ_ERR_UNSUPPORTED, "(N / 64 + B) * H exceeds 2^23");
     *bytes = carve(rule, B, N, backward != 0, nullptr, nullptr);
     return STQ_OK;
 }

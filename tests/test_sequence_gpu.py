@@ -466,6 +466,38 @@ def test_chunk_forward_in_a_graph(stq):
         assert torch.equal(o, o2) and torch.equal(S, S2)
 
 
+def test_chunk_forward_long_in_a_graph(stq):
+    """The segments of a long sequence, captured once and replayed on other starts and values."""
+    rng = np.random.default_rng(6)
+    n, H, d = 3500, 2, 64
+    plan, other = (stq.ChunkPlan(H, d, d, max_tokens=n, max_seqs=2) for _ in range(2))
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    x, _ = _inputs(rng, n, H, d, d, False, True, lo=0.99)
+    names = ("q", "k", "v", "a", "beta")
+    o, S = torch.zeros_like(x["v"]), torch.zeros(1, H, d, d, device="cuda")
+    o2, S2 = torch.zeros_like(o), torch.empty_like(S)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        stq.chunk_forward(plan, cu, *[x[m] for m in names], o, initial_state=S, final_state=S)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stq.chunk_forward(plan, cu, *[x[m] for m in names], o, initial_state=S, final_state=S)
+    for i, length in enumerate((n, 3000, 5, 0)):
+        new, _ = _inputs(rng, n, H, d, d, False, True, lo=0.99)
+        for m in names:
+            x[m].copy_(new[m])
+        cu[1] = length
+        S2.copy_(S)
+        o.fill_(i)
+        o2.fill_(i)
+        stq.chunk_forward(other, cu, *[new[m] for m in names], o2, initial_state=S2, final_state=S2)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
 def test_chunk_python_refusals(stq):
     H, d, n = 2, 64, 5
     x, _ = _inputs(np.random.default_rng(0), n, H, d, d, False, True)
@@ -603,6 +635,39 @@ def test_chunk_backward_against_differences(stq, keyvec):
         want = float((g[m].double() * v).sum())
         # d2's own truncation is a third of its distance from d1
         assert abs(d2 - want) < abs(d1 - d2) + 2 * _chunk_tol(lens) * size / eps
+
+
+@pytest.mark.parametrize("lens,H,dk,dv,keyvec,bf16", [
+    ([70, 3, 200], 16, 128, 128, True, True), ([70, 3, 200], 8, 128, 64, False, True),
+    ([1, 0, 3, 2] * 300, 1, 64, 64, True, False), ([2, 1, 0] * 400, 2, 64, 128, False, True),
+    ([1300], 1, 128, 128, False, False)])
+def test_chunk_many_heads_and_sequences(stq, lens, H, dk, dv, keyvec, bf16):
+    """Heads in groups of eight, more sequences than are put in order, a longer one; on another
+    stream than the current one."""
+    rng = np.random.default_rng(31)
+    at, cu = _cu(lens)
+    n, B = at[-1], len(lens)
+    x, y = _inputs(rng, n, H, dk, dv, keyvec, bf16)
+    S0, dlast = (rng.normal(size=(B, H, dk, dv)).astype(np.float32) for _ in range(2))
+    do = torch.from_numpy(rng.normal(size=(n, H, dv)).astype(np.float32)).to(x["v"].dtype)
+    names = ("q", "k", "v", "a", "beta")
+    first, grad, dout = torch.from_numpy(S0).cuda(), torch.from_numpy(dlast).cuda(), do.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    plan = stq.ChunkPlan(H, dk, dv, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32, max_tokens=n, max_seqs=B,
+                         backward=True)
+    o, last = torch.full_like(x["v"], 7.0), torch.full_like(first, 7.0)
+    torch.cuda.synchronize()
+    stq.chunk_forward(plan, cu, *[x[m] for m in names], o, initial_state=first, final_state=last, stream=side)
+    g = _grads(stq, at, cu, x, keyvec, bf16, first, dout, grad, plan=plan, stream=side)
+    side.synchronize()
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in names), S0)
+    _within(o.double().cpu().numpy(), wo, _chunk_tol(lens) + _io_step(bf16))
+    _within(last.cpu().numpy(), wl, _chunk_tol(lens))
+    want = seqref.backward(at, *(y[m] for m in names), S0, do.double().numpy(), dlast)
+    for m in names:
+        _within(g[m].double().cpu().numpy(), want[m], _grad_tol(m, lens) + _io_step(bf16 and m in "qkv"))
+    _within(g["state"].cpu().numpy(), want["state"], _grad_tol("state", lens))
 
 
 def test_chunk_backward_alone_and_in_a_graph(stq):

@@ -45,7 +45,7 @@ def test_recurrent_refuses_a_rule(stq, bad, status):
     ({"B": -1}, 1), ({"N": -1}, 1), ({"slots": 1}, 1), ({"slots": -1}, 1), ({"cu": None}, 1), ({"q": None}, 1),
     ({"k": None}, 1), ({"v": None}, 1), ({"a": None}, 1), ({"beta": None}, 1), ({"state": None}, 1), ({"o": None}, 1),
     ({"q": P + 8}, 4), ({"o": P + 4}, 4), ({"state": P + 8}, 4), ({"cu": P + 2}, 4), ({"ids": P + 1}, 4),
-    ({"commit": P + 2}, 4)])
+    ({"commit": P + 2}, 4), ({"B": (1 << 18) + 1, "slots": 1 << 19}, 2)])
 def test_recurrent_refuses_arguments(stq, kw, status):
     assert _step(stq, _rule(stq), **kw) == status
     assert stq.library().stq_last_error().decode()
@@ -119,9 +119,10 @@ def test_chunk_refuses_a_rule(stq, bad, status):
     ({"B": -1}, 1), ({"N": -1}, 1), ({"cu": None}, 1), ({"q": None}, 1), ({"k": None}, 1), ({"v": None}, 1),
     ({"a": None}, 1), ({"beta": None}, 1), ({"ws": None}, 1), ({"ws": P + 8}, 4), ({"q": P + 8}, 4), ({"k": P + 4}, 4),
     ({"beta": P + 4}, 4), ({"cu": P + 2}, 4), ({"first": P + 8}, 4), ({"n": 1000}, 3), ({"B": 1 << 29}, 2),
-    ({"B": 1 << 20, "N": (1 << 31) - 1}, 2)])
+    ({"B": (1 << 13) + 1}, 2),
+    ({"N": 64 << 16}, 2), ({"N": (1 << 31) - 1}, 2)])
 def test_chunk_refuses_arguments(stq, kw, status):
-    many = _rule(stq, H=128)             # heads enough for the last two
+    many = _rule(stq, H=128)             # heads enough for the last four
     for call in (_forward, _backward):
         assert call(stq, many, **kw) == status
         assert stq.library().stq_last_error().decode()
