@@ -63,20 +63,22 @@ enum Pass { kForward, kCarry, kSave, kReverse };
 // helps it: four, or two where what the helpers hand over leaves no room for four in LDS.
 template <int DK, bool KEYVEC, bool BF16, Pass PASS>
 struct PassShared {
+    // (Every array on a 128-byte line: a wave's fragment that straddles one takes more cycles.  16 bytes off, the
+    // carrying pass took 363 in place of 217 us.)
     static constexpr int NK = KEYVEC || !BF16 ? 2 : 1, KS = DK / 32, CT = DK / 16;
     static constexpr int NQ = PASS == kForward ? (BF16 ? 1 : 2) : NK;  // parts of Q
     static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (P^T)
     static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse;
     static constexpr int NW = DK == 128 && REV && NK == 2 ? 2 : 4;
-    _Float16 K[NK][4][KS][kFrag];
-    _Float16 Q[FWD ? NQ : 1][FWD ? 4 : 1][FWD ? KS : 1][kFrag];
-    u32x4 T[2 * kPart];                          // T, N' or N^T
-    u32x4 P[FWD || REV ? NP * kPart : 1];        // P or P^T
-    ChunkMeta m[2];                              // of even and of odd steps
-    _Float16 W[NK][CT][2][kFrag];                // K^T
-    _Float16 V[REV ? NQ : 1][REV ? CT : 1][REV ? 2 : 1][kFrag];  // Q^T
+    alignas(128) _Float16 K[NK][4][KS][kFrag];
+    alignas(128) _Float16 Q[FWD ? NQ : 1][FWD ? 4 : 1][FWD ? KS : 1][kFrag];
+    alignas(128) u32x4 T[2 * kPart];                          // T, N' or N^T
+    alignas(128) u32x4 P[FWD || REV ? NP * kPart : 1];        // P or P^T
+    alignas(128) ChunkMeta m[2];                              // of even and of odd steps
+    alignas(128) _Float16 W[NK][CT][2][kFrag];                // K^T
+    alignas(128) _Float16 V[REV ? NQ : 1][REV ? CT : 1][REV ? 2 : 1][kFrag];  // Q^T
     // reverse, helper to carrier: P^T dO and (Q before)^T dO, as result tiles
-    floatx4 pd[REV ? NW : 1][4][REV ? 64 : 1], zd[REV ? NW : 1][REV ? CT : 1][REV ? 64 : 1];
+    alignas(128) floatx4 pd[REV ? NW : 1][4][REV ? 64 : 1], zd[REV ? NW : 1][REV ? CT : 1][REV ? 64 : 1];
 };
 
 // COUNT pieces of 16 bytes, PT threads.
