@@ -79,36 +79,31 @@ stq::SeqArgs seq_args(const stq_rule *r, int32_t B, int32_t N, const int32_t *cu
 // The parts of a chunk workspace at `base`, into *a (both may be NULL); its size.
 size_t carve(const stq_rule *r, int32_t B, int32_t N, bool backward, void *base, stq::ChunkArgs *a) {
     const size_t entries = (size_t)stq::chunk_slots(N, B) * r->H;
-    size_t at = 0;
-    auto take = [&](size_t each) {
-        char *p = static_cast<char *>(base) + at;
-        at += (each * entries + 255) / 256 * 256;
+    size_t at = sizeof(int32_t) * stq::kOrdered;
+    auto take = [&](size_t bytes) -> void * {
+        void *p = base ? static_cast<char *>(base) + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
         return p;
     };
     stq::ChunkArgs none{};
     if (!a) a = &none;
     a->slots = stq::chunk_slots(N, B);
-    at = sizeof(int32_t) * stq::kOrdered;
     a->order = B > 1 && B <= stq::kOrdered ? static_cast<int32_t *>(base) : nullptr;
-    a->prep = reinterpret_cast<stq::ChunkPrep *>(take(sizeof(stq::ChunkPrep)));
-    if (r->gate == STQ_GATE_KEYVEC) a->gates = reinterpret_cast<stq::ChunkGates *>(take(sizeof(stq::ChunkGates)));
+    a->prep = static_cast<stq::ChunkPrep *>(take(sizeof(stq::ChunkPrep) * entries));
+    if (r->gate == STQ_GATE_KEYVEC) a->gates = static_cast<stq::ChunkGates *>(take(sizeof(stq::ChunkGates) * entries));
     const int64_t steps = stq::chunk_steps(r->H, r->d_v, N);
     if (!backward && steps > 0) {
-        auto more = [&](int64_t n, int cols) {
-            float *p = reinterpret_cast<float *>(static_cast<char *>(base) + at);
-            at += (size_t)n * r->d_k * cols * sizeof(float);
-            return p;
-        };
-        a->steps = more(steps, r->d_v + r->d_k);
-        a->starts = more(2 * steps, r->d_v);
+        a->steps = static_cast<float *>(take(sizeof(float) * (size_t)steps * r->d_k * (r->d_v + r->d_k)));
+        a->starts = static_cast<float *>(take(sizeof(float) * (size_t)steps * 2 * r->d_k * r->d_v));
     }
     a->segs = backward ? 1 : stq::chunk_segments(r->H, r->d_k, r->d_v, B, N);
     if (backward) {
-        a->back = reinterpret_cast<stq::ChunkBack *>(take(sizeof(stq::ChunkBack)));
-        a->S = reinterpret_cast<float *>(take(sizeof(float) * r->d_k * r->d_v));
-        a->dS = reinterpret_cast<float *>(take(sizeof(float) * r->d_k * r->d_v));
-        a->w = reinterpret_cast<float *>(take(sizeof(float) * stq::kC * r->d_v));
-        a->y = reinterpret_cast<float *>(take(sizeof(float) * stq::kC * r->d_v));
+        const size_t state = sizeof(float) * r->d_k * r->d_v * entries, rows = sizeof(float) * stq::kC * r->d_v * entries;
+        a->back = static_cast<stq::ChunkBack *>(take(sizeof(stq::ChunkBack) * entries));
+        a->S = static_cast<float *>(take(state));
+        a->dS = static_cast<float *>(take(state));
+        a->w = static_cast<float *>(take(rows));
+        a->y = static_cast<float *>(take(rows));
     }
     return at;
 }
