@@ -190,12 +190,13 @@ __device__ inline void split(float x, float s, _Float16 &hi, _Float16 &lo) {
 }
 
 // Lanes l and l ^ 16, or l ^ 32, exchanged by one vector instruction: both of a pair get
-// both values.
+// both values.  (Values of at least 0 are in the order of their bits; as numbers they would be
+// quieted first, an instruction each, and not fold a value across lanes in.)
 __device__ inline float max_groups(float x) {
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const uint32_t m = max((uint32_t)r[0], (uint32_t)r[1]);
+    r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return __uint_as_float(max((uint32_t)r[0], (uint32_t)r[1]));
 }
 
 // The value of another lane of the row of 16 (`old` where there is none).
@@ -215,12 +216,13 @@ constexpr int quad(int a, int b, int c, int d) { return a | b << 2 | c << 4 | d 
 // inside a branch would find the other lanes switched off.
 __device__ inline float pick(bool c, float x, float y) { return c ? x : y; }
 
-// max over the lanes of a row of 16
+// max over the lanes of a row of 16, of values of at least 0
+template <int ctrl>
+__device__ inline uint32_t max_dpp(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, ctrl, 0xf, 0xf, true));
+}
 __device__ inline float max_row(float x) {
-    x = fmaxf(x, dpp<kRor + 8>(x));
-    x = fmaxf(x, dpp<kRor + 4>(x));
-    x = fmaxf(x, dpp<kRor + 2>(x));
-    return fmaxf(x, dpp<kRor + 1>(x));
+    return __uint_as_float(max_dpp<kRor + 1>(max_dpp<kRor + 2>(max_dpp<kRor + 4>(max_dpp<kRor + 8>(__float_as_uint(x))))));
 }
 // sum over the lanes l, l ^ 16, l ^ 32, l ^ 48
 __device__ inline float sum_groups(float x) {

@@ -605,15 +605,15 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
             for (int r = 0; r < 4; ++r) {
                 const float x = on ? av[r] : 1.f;
                 a[t][r] = x;
-                const float p2 = x * pick(b1, dpp0<quad(0, 0, 2, 2)>(x), 1.f);
-                const float p4 = p2 * pick(b2, dpp0<quad(1, 1, 1, 1)>(p2), 1.f);
+                const float p2 = pick(b1, dpp0<quad(0, 0, 2, 2)>(x) * x, x);
+                const float p4 = pick(b2, dpp0<quad(1, 1, 1, 1)>(p2) * p2, p2);
                 const float t4 = dpp0<quad(3, 3, 3, 3)>(p4);
-                const float p8 = p4 * pick(b4, dpp0<kShr + 4>(t4), 1.f);
-                up[t][r] = p8 * pick(b8, dpp0<kBcast + 7>(p8), 1.f);
+                const float p8 = pick(b4, dpp0<kShr + 4>(t4) * p4, p4);
+                up[t][r] = pick(b8, dpp0<kBcast + 7>(p8) * p8, p8);
                 float f = pick(b1, 1.f, dpp0<quad(1, 1, 3, 3)>(x));
-                f *= pick(b2, 1.f, dpp0<quad(3, 3, 3, 3)>(p2));
-                f *= pick(b4, 1.f, dpp0<kShl + 4>(t4));
-                past[t][r] = f * pick(b8, 1.f, dpp0<kBcast + 15>(p8));
+                f = pick(b2, f, dpp0<quad(3, 3, 3, 3)>(p2) * f);
+                f = pick(b4, f, dpp0<kShl + 4>(t4) * f);
+                past[t][r] = pick(b8, f, dpp0<kBcast + 15>(p8) * f);
                 ks[r] = k[t][r] * past[t][r];
                 kp[r] = k[t][r] * up[t][r];
                 qp[r] = q[t][r] * up[t][r];

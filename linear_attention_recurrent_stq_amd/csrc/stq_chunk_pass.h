@@ -179,8 +179,8 @@ struct Producer {
             widen(k[i], kx);
             if constexpr (kQ) widen(q[kQ ? i : 0], qx);
             if constexpr (KEYVEC) {
-                float x[4];
-                gate(i, x);
+                float x[4];              // (of a token past the last one too: its row is not used)
+                widen(a[i], x);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) before[c] *= x[c];
             }
@@ -189,11 +189,13 @@ struct Producer {
             for (int c = 0; c < 4; ++c) {
                 _Float16 hi, lo;
                 if constexpr (NK == 2) {
-                    const float b = KEYVEC ? kx[c] * before[c] : kx[c], f = KEYVEC ? kx[c] * after[i][c] : kx[c];
-                    split(REV ? f : b, ek[i], hi, lo);
+                    // (ek is a power of two; the reverse pass, short of registers, spills where it comes first)
+                    const float s = REV ? kx[c] : kx[c] * ek[i], rest = REV ? ek[i] : 1.f;
+                    const float b = KEYVEC ? s * before[c] : s, f = KEYVEC ? s * after[i][c] : s;
+                    split(REV ? f : b, rest, hi, lo);
                     kh[c] = hi;
                     kl[c] = lo;
-                    if constexpr (KEYVEC) split(REV ? b : f, ek[i], hi, lo);
+                    if constexpr (KEYVEC) split(REV ? b : f, rest, hi, lo);
                     w[0][c][i] = hi;
                     w[NK - 1][c][i] = lo;
                 } else {

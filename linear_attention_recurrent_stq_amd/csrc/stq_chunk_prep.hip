@@ -64,7 +64,8 @@ struct Rows {
 };
 
 // A 16x16 result tile times its rows' scales s, as fp16 pairs in fragment order;
-// tile (I, J) of a lower triangular matrix.
+// tile (I, J) of a lower triangular matrix.  LO: with the lo part.
+template <bool LO>
 __device__ inline void store_tile(floatx4 x, floatx4 s, int I, int J, uint16_t (&to)[2][kTri][kFrag]) {
     const int c16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     float y[4];
@@ -80,7 +81,7 @@ __device__ inline void store_tile(floatx4 x, floatx4 s, int I, int J, uint16_t (
     const int f = I < 2 ? I : 2 + 2 * (I - 2) + (J >> 1);
     const int at = (4 * g + (c16 & 3) + 16 * (c16 >> 2)) * 8 + (J & 1) * 4;
     *reinterpret_cast<half4 *>(&to[0][f][at]) = hi;
-    *reinterpret_cast<half4 *>(&to[1][f][at]) = lo;
+    if constexpr (LO) *reinterpret_cast<half4 *>(&to[1][f][at]) = lo;
 }
 
 // The transpose of tile (I, J) times its rows' scale s (columns of the tile): a lane
@@ -123,7 +124,8 @@ __device__ inline void store_pt(const floatx4 (&p)[4], float (*tm)[kC], ChunkMet
     __syncthreads();
 }
 
-// Row w of P's blocks.
+// Row w of P's blocks.  LO: for fp32 outputs; bf16 ones take the hi part alone.
+template <bool LO>
 __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
     const int lane = threadIdx.x & 63, w = wave_index(), c16 = lane & 15, g = lane >> 4;
     floatx4 s, inv;
@@ -137,7 +139,7 @@ __device__ inline void store_p(const floatx4 (&p)[4], ChunkPrep &out) {
     }
 #pragma unroll
     for (int J = 0; J < 4; ++J)
-        if (J <= (w | 1)) store_tile(J <= w ? p[J] : floatx4{0.f, 0.f, 0.f, 0.f}, s, w, J, out.P);
+        if (J <= (w | 1)) store_tile<LO>(J <= w ? p[J] : floatx4{0.f, 0.f, 0.f, 0.f}, s, w, J, out.P);
     if (c16 == 0) *reinterpret_cast<floatx4 *>(&out.m.rp[16 * w + 4 * g]) = inv;
 }
 
@@ -245,7 +247,7 @@ __device__ inline void store_t(float (*M)[LD], float (*X)[20], float (*tm)[kC], 
             s[r] = scale_to(m[r], 10, x);
             inv[r] = x;
         }
-        store_tile(t[I], s, I, wave, out.T);
+        store_tile<true>(t[I], s, I, wave, out.T);
         if (I == wave && j == 0) *reinterpret_cast<floatx4 *>(&out.m.rt[16 * I + 4 * g]) = inv;
     }
 }
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
         back = A.back + (size_t)slot * s.H + h;
         store_pt(pp, tm, out.m, *back);
     } else {
-        store_p(pp, out);
+        store_p<!BF16>(pp, out);
     }
     __syncthreads();
     store_t<BACK>(big.M, X, tm, be, aa, out, back);
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
         out.m.rq[row] = x.iq;
     }
     const bool b1 = c16 & 1, b2 = c16 & 2, b4 = c16 & 4, b8 = c16 & 8, on = row < n;
-    float kp[KS][8], qp[KS][8];      // k pre, q pre
+    float kp[KS][8], qp[KS][8];      // k pre, q pre, scaled
     floatx4 cut4 = {0.f, 0.f, 0.f, 0.f}, cut8 = cut4;
     float da[3] = {}, dq[4] = {};    // 4x4 blocks: rows d earlier, A for d = 1, 2, 3 and P for d = 0 .. 3
     floatx4 n0 = four(s.a + x.at), n1 = four(s.a + x.at + 4);  // the next channels' gates
@@ -457,23 +459,25 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
             da[2] = __builtin_fmaf(k, v, da[2]);
             dq[3] = __builtin_fmaf(q, v, dq[3]);
             // products within 2, 4, 8 and 16 rows: up to the row (p), after it (f)
-            const float p2 = a * pick(b1, dpp0<quad(0, 0, 2, 2)>(a), 1.f);
-            const float p4 = p2 * pick(b2, dpp0<quad(1, 1, 1, 1)>(p2), 1.f);
+            // (the value across lanes is multiplied first and chosen then: it folds into the product)
+            const float p2 = pick(b1, dpp0<quad(0, 0, 2, 2)>(a) * a, a);
+            const float p4 = pick(b2, dpp0<quad(1, 1, 1, 1)>(p2) * p2, p2);
             const float t4 = dpp0<quad(3, 3, 3, 3)>(p4);
-            const float p8 = p4 * pick(b4, dpp0<kShr + 4>(t4), 1.f);
-            const float p16 = p8 * pick(b8, dpp0<kBcast + 7>(p8), 1.f);
+            const float p8 = pick(b4, dpp0<kShr + 4>(t4) * p4, p4);
+            const float p16 = pick(b8, dpp0<kBcast + 7>(p8) * p8, p8);
+            const float ks = k * x.sk, qs = q * x.sq;  // (powers of two)
             float f = pick(b1, 1.f, dpp0<quad(1, 1, 3, 3)>(a));
-            f *= pick(b2, 1.f, dpp0<quad(3, 3, 3, 3)>(p2));
-            y4[e] = k * f;
-            f *= pick(b4, 1.f, dpp0<kShl + 4>(t4));
-            y8[e] = k * f;
-            f *= pick(b8, 1.f, dpp0<kBcast + 15>(p8));
-            y16[e] = k * f;
+            f = pick(b2, f, dpp0<quad(3, 3, 3, 3)>(p2) * f);
+            y4[e] = ks * f;
+            f = pick(b4, f, dpp0<kShl + 4>(t4) * f);
+            y8[e] = ks * f;
+            f = pick(b8, f, dpp0<kBcast + 15>(p8) * f);
+            y16[e] = ks * f;
             // the later half's rows of K, and of Q in the rows that the earlier half leaves free
-            z4[e] = pick(b4, k * p4 * x.sk, dpp0<kShl + 4>(q * p4 * x.sq));
-            z8[e] = pick(b8, k * p8 * x.sk, dpp0<kShl + 8>(q * p8 * x.sq));
-            kp[i][e] = k * p16;
-            qp[i][e] = q * p16;
+            z4[e] = pick(b4, ks * p4, dpp0<kShl + 4>(qs * p4));
+            z8[e] = pick(b8, ks * p8, dpp0<kShl + 8>(qs * p8));
+            kp[i][e] = ks * p16;
+            qp[i][e] = qs * p16;
             asm volatile("" : "+v"(kp[i][e]), "+v"(qp[i][e]));  // (formed here, not where a wave uses them)
             pe[e >> 2][e & 3] = p16;
             fe[e >> 2][e & 3] = f;
@@ -489,13 +493,13 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
         }
         half8 zh, zl, yh, yl;
         split8(z4, 1.f, zh, zl);
-        split8(y4, x.sk, yh, yl);
+        split8(y4, 1.f, yh, yl);
         cut4 = mfma_pairs(zh, zl, yh, yl, cut4);
         split8(z8, 1.f, zh, zl);
-        split8(y8, x.sk, yh, yl);
+        split8(y8, 1.f, yh, yl);
         cut8 = mfma_pairs(zh, zl, yh, yl, cut8);
         if (w < 3) {
-            split8(y16, x.sk, yh, yl);
+            split8(y16, 1.f, yh, yl);
             Y[w][i][0][lane] = yh;
             Y[w][i][1][lane] = yl;
         }
@@ -541,9 +545,9 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
             }
             const half8 yh = Y[J][i][0][lane], yl = Y[J][i][1][lane];
             half8 zh, zl;
-            split8(kp[i], x.sk, zh, zl);
+            split8(kp[i], 1.f, zh, zl);
             aa[J] = mfma_pairs(zh, zl, yh, yl, aa[J]);
-            split8(qp[i], x.sq, zh, zl);
+            split8(qp[i], 1.f, zh, zl);
             pp[J] = mfma_pairs(zh, zl, yh, yl, pp[J]);
         }
     }
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
         back = A.back + (size_t)slot * s.H + h;
         store_pt(pp, tm, out.m, *back);
     } else {
-        store_p(pp, out);
+        store_p<!BF16>(pp, out);
     }
     __syncthreads();
     store_t<BACK>(big.M, X, tm, be, aa, out, back);
