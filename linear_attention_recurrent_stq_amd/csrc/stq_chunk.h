@@ -188,6 +188,14 @@ __device__ inline void split(float x, float s, _Float16 &hi, _Float16 &lo) {
     hi = (_Float16)(x * s);
     lo = (_Float16)__builtin_fmaf(x, s, -(float)hi);
 }
+// x, scaled already, as hi + lo.  (The 1 is hidden from the compiler: x - hi would be three
+// instructions, the mixed product and sum with its rounding is one.)
+__device__ inline void split(float x, _Float16 &hi, _Float16 &lo) {
+    float one = 1.f;
+    asm("" : "+s"(one));
+    hi = (_Float16)x;
+    lo = (_Float16)__builtin_fmaf(x, one, -(float)hi);
+}
 
 // Lanes l and l ^ 16, or l ^ 32, exchanged by one vector instruction: both of a pair get
 // both values.  (Values of at least 0 are in the order of their bits; as numbers they would be
@@ -252,6 +260,15 @@ template <> struct Row8<false> {
     __device__ float get(int i) const { return i < 4 ? x[i] : y[i - 4]; }
 };
 
+__device__ inline void split8(const float (&x)[8], half8 &hi, half8 &lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        _Float16 a, b;
+        split(x[e], a, b);
+        hi[e] = a;
+        lo[e] = b;
+    }
+}
 // x s of eight channels as fp16 pairs
 __device__ inline void split8(const float (&x)[8], float s, half8 &hi, half8 &lo) {
 #pragma unroll

@@ -475,8 +475,10 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
             half4 hi, lo;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                hi[r] = (_Float16)y[r];
-                lo[r] = (_Float16)(y[r] - (float)hi[r]);
+                _Float16 a, b;
+                split(y[r], a, b);
+                hi[r] = a;
+                lo[r] = b;
             }
             reinterpret_cast<half4 *>(&to[0][ct][w >> 1][turned])[w & 1] = hi;
             if constexpr (NK == 2) reinterpret_cast<half4 *>(&to[NK - 1][ct][w >> 1][turned])[w & 1] = lo;
@@ -590,8 +592,10 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
             half4 hi, lo;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                hi[r] = (_Float16)y[r];
-                lo[r] = (_Float16)(y[r] - (float)hi[r]);
+                _Float16 a, b;
+                split(y[r], a, b);
+                hi[r] = a;
+                lo[r] = b;
             }
             to[0][ct][w][turned] = hi;
             to[1][ct][w][turned] = lo;

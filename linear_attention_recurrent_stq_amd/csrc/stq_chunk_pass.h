@@ -190,12 +190,14 @@ struct Producer {
                 _Float16 hi, lo;
                 if constexpr (NK == 2) {
                     // (ek is a power of two; the reverse pass, short of registers, spills where it comes first)
-                    const float s = REV ? kx[c] : kx[c] * ek[i], rest = REV ? ek[i] : 1.f;
+                    const float s = REV ? kx[c] : kx[c] * ek[i];
                     const float b = KEYVEC ? s * before[c] : s, f = KEYVEC ? s * after[i][c] : s;
-                    split(REV ? f : b, rest, hi, lo);
+                    if constexpr (REV) split(f, ek[i], hi, lo);
+                    else split(b, hi, lo);
                     kh[c] = hi;
                     kl[c] = lo;
-                    if constexpr (KEYVEC) split(REV ? b : f, rest, hi, lo);
+                    if constexpr (KEYVEC && REV) split(b, ek[i], hi, lo);
+                    else if constexpr (KEYVEC) split(f, hi, lo);
                     w[0][c][i] = hi;
                     w[NK - 1][c][i] = lo;
                 } else {

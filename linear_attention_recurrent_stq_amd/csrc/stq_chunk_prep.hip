@@ -75,8 +75,10 @@ __device__ inline void store_tile(floatx4 x, floatx4 s, int I, int J, uint16_t (
     half4 hi, lo;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        hi[r] = (_Float16)y[r];
-        lo[r] = (_Float16)(y[r] - (float)hi[r]);
+        _Float16 a, b;
+        split(y[r], a, b);
+        hi[r] = a;
+        lo[r] = b;
     }
     const int f = I < 2 ? I : 2 + 2 * (I - 2) + (J >> 1);
     const int at = (4 * g + (c16 & 3) + 16 * (c16 >> 2)) * 8 + (J & 1) * 4;
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
 }
 
 template <int DK, bool BF16, bool BACK>
-__global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
+__global__ void __launch_bounds__(256, 2) k_prep_keyvec(const ChunkArgs A) {
     constexpr int KS = DK / 32;
     __shared__ union {
         float M[kC][LD];
@@ -492,14 +494,14 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
             }
         }
         half8 zh, zl, yh, yl;
-        split8(z4, 1.f, zh, zl);
-        split8(y4, 1.f, yh, yl);
+        split8(z4, zh, zl);
+        split8(y4, yh, yl);
         cut4 = mfma_pairs(zh, zl, yh, yl, cut4);
-        split8(z8, 1.f, zh, zl);
-        split8(y8, 1.f, yh, yl);
+        split8(z8, zh, zl);
+        split8(y8, yh, yl);
         cut8 = mfma_pairs(zh, zl, yh, yl, cut8);
         if (w < 3) {
-            split8(y16, 1.f, yh, yl);
+            split8(y16, yh, yl);
             Y[w][i][0][lane] = yh;
             Y[w][i][1][lane] = yl;
         }
@@ -545,9 +547,9 @@ __global__ void __launch_bounds__(256, 4) k_prep_keyvec(const ChunkArgs A) {
             }
             const half8 yh = Y[J][i][0][lane], yl = Y[J][i][1][lane];
             half8 zh, zl;
-            split8(kp[i], 1.f, zh, zl);
+            split8(kp[i], zh, zl);
             aa[J] = mfma_pairs(zh, zl, yh, yl, aa[J]);
-            split8(qp[i], 1.f, zh, zl);
+            split8(qp[i], zh, zl);
             pp[J] = mfma_pairs(zh, zl, yh, yl, pp[J]);
         }
     }
