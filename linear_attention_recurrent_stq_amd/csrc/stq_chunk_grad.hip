@@ -76,7 +76,7 @@ struct GradShared {
             half4 y[2][CT][4][64], x[2][CT][4][64], z[2][CT][4][64];      // (K suf)^T, (K pre)^T, (Q pre)^T
         } v;
     };
-    float iw[kC], iy[kC], io[kC], ik[kC], iq[kC], be[kC], ga[kC], pre[kC], suf[kC];
+    alignas(16) float iw[kC], iy[kC], io[kC], ik[kC], iq[kC], be[kC], ga[kC], pre[kC], suf[kC];
     float srow[DK], rho[DK];             // scales of a state's rows; sum over v of dS S
     float B[4][DK];                      // key-vector gates: products of the blocks
     float d[2][4][16][17];               // key-vector gates: dP, dA inside the blocks [i][j]
@@ -374,16 +374,19 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
     {
         float near[2][4] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};  // scalar decays inside the block
         if constexpr (!KEYVEC) {
+            floatx4 gate[4];             // (read by all lanes: a choice of loads would be a branch each)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gate[i] = four(&sh.ga[16 * w + 4 * i]);
             float run = 1.f;             // rows j before the own token
 #pragma unroll
             for (int j = 15; j >= 0; --j) {
-                if (j < 15) run *= j < c16 ? sh.ga[16 * w + j + 1] : 1.f;
+                if (j < 15) run *= j < c16 ? gate[(j + 1) >> 2][(j + 1) & 3] : 1.f;
                 near[0][j & 3] = j >> 2 == g ? run : near[0][j & 3];
             }
             run = 1.f;                   // rows i behind it
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                run *= i > c16 ? sh.ga[16 * w + i] : 1.f;
+                run *= i > c16 ? gate[i >> 2][i & 3] : 1.f;
                 near[1][i & 3] = i >> 2 == g ? run : near[1][i & 3];
             }
         }
@@ -403,13 +406,15 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
 #pragma unroll
                     for (int x = 1; x < 3; ++x) d *= x > J && x < w ? gB[x] : 1.f;
                 }
+                const floatx4 be = four(&sh.be[16 * J + 4 * g]), iw = four(&sh.iw[16 * J + 4 * g]),
+                              suf = KEYVEC ? be : four(&sh.suf[16 * J + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int j = 16 * J + 4 * g + r;
-                    float f = sh.be[j] * d;
-                    if constexpr (!KEYVEC) f *= J < w ? sh.suf[j] : near[0][r];
-                    PT[J][r] = J < w || 4 * g + r <= c16 ? (PT[J][r] * sh.iw[j] * own_io) * f : 0.f;
-                    AT[J][r] = J < w || 4 * g + r < c16 ? -(AT[J][r] * sh.iw[j] * own_iy) * (f * own_be) : 0.f;
+                    float f = be[r] * d;
+                    if constexpr (!KEYVEC) f *= J < w ? suf[r] : near[0][r];
+                    const float p = (PT[J][r] * iw[r] * own_io) * f, a = -(AT[J][r] * iw[r] * own_iy) * (f * own_be);
+                    PT[J][r] = J < w || 4 * g + r <= c16 ? p : 0.f;
+                    AT[J][r] = J < w || 4 * g + r < c16 ? a : 0.f;
                 }
             }
             if (J >= w) {
@@ -425,13 +430,15 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
 #pragma unroll
                     for (int x = 1; x < 3; ++x) d *= x > w && x < J ? gB[x] : 1.f;
                 }
+                const floatx4 be = four(&sh.be[16 * J + 4 * g]), io = four(&sh.io[16 * J + 4 * g]),
+                              iy = four(&sh.iy[16 * J + 4 * g]), pre = KEYVEC ? be : four(&sh.pre[16 * J + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * J + 4 * g + r;
                     float f = d;
-                    if constexpr (!KEYVEC) f *= J > w ? sh.pre[i] : near[1][r];
-                    PF[J][r] = J > w || 4 * g + r >= c16 ? (PF[J][r] * sh.io[i] * own_iw) * f : 0.f;
-                    AF[J][r] = J > w || 4 * g + r > c16 ? -(AF[J][r] * sh.iy[i] * own_iw) * (f * sh.be[i]) : 0.f;
+                    if constexpr (!KEYVEC) f *= J > w ? pre[r] : near[1][r];
+                    const float p = (PF[J][r] * io[r] * own_iw) * f, a = -(AF[J][r] * iy[r] * own_iw) * (f * be[r]);
+                    PF[J][r] = J > w || 4 * g + r >= c16 ? p : 0.f;
+                    AF[J][r] = J > w || 4 * g + r > c16 ? a : 0.f;
                 }
             }
         }

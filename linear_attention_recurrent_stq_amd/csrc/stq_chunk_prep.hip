@@ -355,9 +355,12 @@ __global__ void __launch_bounds__(256) k_prep_scalar(const ChunkArgs A) {
     floatx4 dd;                      // decay inside the diagonal block
     {
         float run = 1.f;
+        floatx4 gate[4];             // (read by all lanes: a choice of loads would be a branch each)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gate[i] = four(&ga[16 * wave + 4 * i]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            run *= i > c16 ? ga[16 * wave + i] : 1.f;
+            run *= i > c16 ? gate[i >> 2][i & 3] : 1.f;
             dd[i & 3] = i >> 2 == g ? run : i < 4 ? 1.f : dd[i & 3];
         }
     }
