@@ -189,10 +189,13 @@ __device__ inline void split(float x, float s, _Float16 &hi, _Float16 &lo) {
     lo = (_Float16)__builtin_fmaf(x, s, -(float)hi);
 }
 // x, scaled already, as hi + lo.  (The 1 is hidden from the compiler: x - hi would be three
-// instructions, the mixed product and sum with its rounding is one.)
+// instructions, the mixed product and sum with its rounding is one.  So is where x comes from: a product
+// is else rounded to hi at once in one place, and by way of fp32 in the other, and the two differ now and
+// then by a step of fp16.)
 __device__ inline void split(float x, _Float16 &hi, _Float16 &lo) {
     float one = 1.f;
     asm("" : "+s"(one));
+    asm("" : "+v"(x));
     hi = (_Float16)x;
     lo = (_Float16)__builtin_fmaf(x, one, -(float)hi);
 }
@@ -260,13 +263,21 @@ template <> struct Row8<false> {
     __device__ float get(int i) const { return i < 4 ? x[i] : y[i - 4]; }
 };
 
+// Eight of them (hi parts are rounded two at a time).
 __device__ inline void split8(const float (&x)[8], half8 &hi, half8 &lo) {
+    typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    float one = 1.f;
+    asm("" : "+s"(one));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        _Float16 a, b;
-        split(x[e], a, b);
-        hi[e] = a;
-        lo[e] = b;
+    for (int e = 0; e < 8; e += 2) {
+        float a = x[e], b = x[e + 1];
+        asm("" : "+v"(a), "+v"(b));
+        const half2 h = __builtin_convertvector((floatx2{a, b}), half2);
+        hi[e] = h[0];
+        hi[e + 1] = h[1];
+        lo[e] = (_Float16)__builtin_fmaf(a, one, -(float)h[0]);
+        lo[e + 1] = (_Float16)__builtin_fmaf(b, one, -(float)h[1]);
     }
 }
 // x s of eight channels as fp16 pairs

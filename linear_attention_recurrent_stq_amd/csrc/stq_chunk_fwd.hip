@@ -25,9 +25,9 @@
 // turned within quads of lanes.
 //
 // Measured, bf16, d_k = d_v = 128, MI355X: scalar gates, 24 ragged sequences of 24000 tokens, 32
-// heads 485 us; key-vector gates, 40 of 16001 tokens, 32 heads 407 us.  One sequence of 16384
-// tokens, 16 heads, key-vector gates: 1063 us in one go (32 workgroups); in 5 segments 222 us for
-// the segments' states and matrices, 14 us to join them, 278 us for the outputs.
+// heads 492 us; key-vector gates, 40 of 16001 tokens, 32 heads 402 us.  One sequence of 16384
+// tokens, 16 heads, key-vector gates: 1063 us in one go (32 workgroups); in 5 segments 202 us for
+// the segments' states and matrices, 14 us to join them, 256 us for the outputs.
 
 #include "stq_chunk_pass.h"
 

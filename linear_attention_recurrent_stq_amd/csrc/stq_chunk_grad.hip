@@ -25,8 +25,10 @@
 // one step of the sum and the next); inside a block each of the fifteen distances is vector
 // code, the other token read across the lanes of a row of 16.
 //
-// A workgroup holds about 110 KB of LDS and eight waves; the bound is the reading of S, dS, w and
-// y (200 KB a chunk at 128 x 128) and, with key-vector gates, the vector code.
+// A workgroup holds about 117 KB of LDS and eight waves of 200 to 256 registers, so one a CU: the bound
+// is its vector instructions (49 % of the cycles with scalar gates, 57 % with key-vector ones) and
+// what they wait for. Measured, bf16, d_k = d_v = 128, 16 heads, MI355X: scalar gates, 16384 tokens 486 us
+// (887 MB, S and dS most of it: 1.8 TB/s); key-vector gates, 8192 tokens 360 us.
 
 #include "stq_chunk.h"
 
@@ -78,9 +80,9 @@ struct GradShared {
     };
     alignas(16) float iw[kC], iy[kC], io[kC], ik[kC], iq[kC], be[kC], ga[kC], pre[kC], suf[kC];
     float srow[DK], rho[DK];             // scales of a state's rows; sum over v of dS S
-    float B[4][DK];                      // key-vector gates: products of the blocks
+    alignas(16) float B[4][DK];          // key-vector gates: products of the blocks
     float d[2][4][16][17];               // key-vector gates: dP, dA inside the blocks [i][j]
-    float te[4][DK], tf[4][DK];          // key-vector gates: sums of e and f of the blocks
+    alignas(16) float te[4][DK], tf[4][DK];  // key-vector gates: sums of e and f of the blocks
     float es[2][kC], fs[2][kC];          // scalar gates: e and f by halves of the channels
 };
 
@@ -628,8 +630,9 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
                 ks[r] = k[t][r] * past[t][r];
                 kp[r] = k[t][r] * up[t][r];
                 qp[r] = q[t][r] * up[t][r];
-                if (c16 == 15) sh.B[w][16 * ct + 4 * g + r] = up[t][r];
             }
+            if (c16 == 15)
+                *reinterpret_cast<floatx4 *>(&sh.B[w][16 * ct + 4 * g]) = floatx4{up[t][0], up[t][1], up[t][2], up[t][3]};
             turn(ks, sk, sh.v.y, ct);
             turn(kp, sk, sh.v.x, ct);
             turn(qp, sq, sh.v.z, ct);
@@ -718,6 +721,7 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
         for (int t = 0; t < T; ++t) {
             const int ct = half * T + t;
             float all[4];
+            floatx4 se, sf;              // sums over the block
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 all[r] = dr[t][r] + dwr[t][r] + vw[t][r];
@@ -733,10 +737,12 @@ __global__ void __launch_bounds__(512) k_chunk_grad(const ChunkArgs A) {
                 y += dpp0<kShr + 2>(y);
                 y += dpp0<kShr + 4>(y);
                 y += dpp0<kShr + 8>(y);
-                if (c16 == 0) sh.te[w][16 * ct + 4 * g + r] = x;
-                if (c16 == 15) sh.tf[w][16 * ct + 4 * g + r] = y;
+                se[r] = x;
+                sf[r] = y;
                 f[t][r] = dpp0<kShr + 1>(y);
             }
+            if (c16 == 0) *reinterpret_cast<floatx4 *>(&sh.te[w][16 * ct + 4 * g]) = se;
+            if (c16 == 15) *reinterpret_cast<floatx4 *>(&sh.tf[w][16 * ct + 4 * g]) = sf;
             store(A.dq, t, dq[t]);
             store(A.dk, t, all);
         }

@@ -565,6 +565,35 @@ def test_chunk_backward(stq, lens, dk, dv, keyvec, bf16):
         _within(g["state"].cpu().numpy(), want["state"], _grad_tol("state", lens))
 
 
+# What the pairs must keep, as a root mean square: over many elements errors are independent.  A
+# value's error as hi + lo is at most 2^-22 of it, evenly spread: 2^-22.8; two operands, the
+# product of the lo parts that is left out (2^-23.6) and a sum of 128 terms in fp32 (2^-22.5):
+# 2^-21.4 a product.  Six stand one behind another in a state or output, twelve in a gradient.
+@pytest.mark.parametrize("keyvec,bf16", [(False, False), (False, True), (True, False), (True, True)])
+def test_chunk_keeps_22_bits(stq, keyvec, bf16):
+    rng = np.random.default_rng(17)
+    n, H, d = 256, 2, 128
+    at, cu = _cu([n])
+    x, y = _inputs(rng, n, H, d, d, keyvec, bf16)
+    names = ("q", "k", "v", "a", "beta")
+    zero = np.zeros((1, H, d, d))
+    plan = stq.ChunkPlan(H, d, d, gate=int(keyvec), io_dtype=stq.BF16 if bf16 else stq.F32, max_tokens=n, max_seqs=1,
+                         backward=True)
+    o, last = torch.empty_like(x["v"]), torch.empty(1, H, d, d, device="cuda")
+    stq.chunk_forward(plan, cu, *[x[m] for m in names], o, final_state=last)
+    wo, wl, _ = seqref.forward(at, *(y[m] for m in names), zero)
+    _within(last.cpu().numpy(), wl, 6 ** 0.5 * 2.0 ** -21.4)
+    do = torch.from_numpy(rng.normal(size=(n, H, d)).astype(np.float32)).to(x["v"].dtype)
+    g = _grads(stq, at, cu, x, keyvec, bf16, None, do.cuda(), None, plan=plan)
+    want = seqref.backward(at, *(y[m] for m in names), zero, do.double().numpy(), zero)
+    for m in ("beta", "state"):
+        _within(g[m].double().cpu().numpy(), want[m], 12 ** 0.5 * 2.0 ** -21.4)
+    if not bf16:
+        _within(o.double().cpu().numpy(), wo, 6 ** 0.5 * 2.0 ** -21.4)
+        for m in ("q", "k", "v"):
+            _within(g[m].double().cpu().numpy(), want[m], 12 ** 0.5 * 2.0 ** -21.4)
+
+
 @pytest.mark.parametrize("keyvec", [False, True])
 @pytest.mark.parametrize("what", ["strong", "beta0", "tiny", "same keys", "zero"])
 def test_chunk_backward_extremes(stq, keyvec, what):
