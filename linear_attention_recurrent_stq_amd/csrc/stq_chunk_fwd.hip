@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_fwd(const ChunkArgs A) {
         if (nc == 0) return;
         Producer<DK, KEYVEC, BF16, PASS> p;
         p.tid = threadIdx.x - 256;
-        p.run(A, sh, h, t0, t1, nc, entry0);
+        const uint32_t row_step = (uint32_t)(H * DV / 4);
+        p.run(A, sh, h, t0, t1, nc, entry0,
+              Shared::OUT ? static_cast<raw *>(A.o) + (size_t)t0 * row_step + (size_t)h * (DV / 4) + part * Shared::GC
+                          : nullptr,
+              row_step);
         return;
     }
 
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_fwd(const ChunkArgs A) {
     asm volatile("" : "+v"(at0));        // (what is formed from it for the last states is formed there)
 
     // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
-    const int row0 = 4 * g + (c16 & 3);
+    const int row0 = 4 * g + (c16 & 3), out0 = slab_at<Shared::GC>(row0, 4 * wave + (c16 >> 2));
     const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
     const size_t col4 = (size_t)h * (DV / 4) + col0 / 4 + (c16 >> 2);
     raw v[4];                            // of the next chunk; past the last token its row again
@@ -245,7 +249,8 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_fwd(const ChunkArgs A) {
                 quad_transpose(x);
                 raw z;
                 narrow(x, z);
-                if (16 * rt + row0 < n) out[(uint32_t)(16 * rt + row0) * row_step] = z;
+                if constexpr (Shared::OUT) sh.out[out0 + 16 * Shared::GC * rt] = z;
+                else if (16 * rt + row0 < n) out[(uint32_t)(16 * rt + row0) * row_step] = z;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -267,6 +272,7 @@ __global__ void __launch_bounds__(256 + 4 * DK) k_chunk_fwd(const ChunkArgs A) {
             for (int r = 0; r < 4; ++r) S[ct][r] = __builtin_fmaf(z[r], undo, S[ct][r] * d[r]);
         });
     }
+    if (Shared::OUT && nc) lds_barrier();  // the last rows are stored
     if constexpr (CARRY) {
         float *to = A.steps + (head * runs + j) * (DK * (DV + DK)) + col0;
         uint32_t at = 4 * g * (DV + DK) + c16;

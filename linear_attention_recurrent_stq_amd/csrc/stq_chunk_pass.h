@@ -70,6 +70,8 @@ struct PassShared {
     static constexpr int NP = PASS == kForward ? NQ : 2;               // parts of P (P^T)
     static constexpr bool FWD = PASS == kForward, REV = PASS == kReverse;
     static constexpr int NW = DK == 128 && REV && NK == 2 ? 2 : 4;
+    static constexpr int GC = 4 * NW;            // groups of four columns
+    static constexpr bool OUT = BF16 && (FWD || REV);  // (see slab_at)
     alignas(128) _Float16 K[NK][4][KS][kFrag];
     alignas(128) _Float16 Q[FWD ? NQ : 1][FWD ? 4 : 1][FWD ? KS : 1][kFrag];
     alignas(128) u32x4 T[2 * kPart];                          // T, N' or N^T
@@ -79,6 +81,7 @@ struct PassShared {
     alignas(128) _Float16 V[REV ? NQ : 1][REV ? CT : 1][REV ? 2 : 1][kFrag];  // Q^T
     // reverse, helper to carrier: P^T dO and (Q before)^T dO, as result tiles
     alignas(128) floatx4 pd[REV ? NW : 1][4][REV ? 64 : 1], zd[REV ? NW : 1][REV ? CT : 1][REV ? 64 : 1];
+    alignas(128) typename Raw4<BF16>::type out[OUT ? kC * GC : 1];  // o or dv, on their way out
 };
 
 // COUNT pieces of 16 bytes, PT threads.
@@ -98,6 +101,17 @@ struct Pieces {
     }
 };
 
+// bf16 outputs go through LDS: a lane has four columns of a row, and the producing threads store whole
+// rows of the workgroup's columns, 16 bytes each.  (A wave's own 16 columns are 32 bytes of a row; stored
+// from there they held up the chain for 3000 to 4000 of a step's 10000 cycles.  Measured: scalar gates, forward of 24000
+// tokens 708 -> 684 us, backward of 16384 1238 -> 1208 us; key-vector gates the same.  Of fp32 rows they are
+// 64 bytes, and it loses: backward of 700 tokens 95 -> 103 us.)  Groups of four columns are
+// exchanged in pairs, so that 16 rows of one group spread over the banks.
+template <int GC>
+__device__ inline int slab_at(int row, int group) {
+    return row * GC + (group ^ (2 * row & (GC - 1)));
+}
+
 // The producing waves: 4 DK threads; a thread takes 4 tokens x 4 channels.
 template <int DK, bool KEYVEC, bool BF16, Pass PASS>
 struct Producer {
@@ -114,6 +128,23 @@ struct Producer {
     half4 w[NK][4];                  // K^T of the chunk whose A half is written
     int n;                           // tokens of the chunk in k, q and a
     int tid, cg, tg;
+
+    // The workgroup's columns of the first `count` rows of a chunk, row_step groups of four apart.
+    __device__ inline void store_out(const Shared &sh, raw *rows, uint32_t row_step, int count) {
+        constexpr int per = BF16 ? 2 : 1, GC = Shared::GC, pieces = kC * GC / per;  // groups in 16 bytes
+        constexpr int each = (pieces + PT - 1) / PT;
+        u32x4 x[each];
+#pragma unroll
+        for (int i = 0; i < each; ++i) {
+            const int p = i * PT + tid, row = p / (GC / per), group = p % (GC / per) * per;
+            if ((i + 1) * PT <= pieces || p < pieces) x[i] = *reinterpret_cast<const u32x4 *>(&sh.out[slab_at<GC>(row, group)]);
+        }
+#pragma unroll
+        for (int i = 0; i < each; ++i) {
+            const int p = i * PT + tid, row = p / (GC / per), group = p % (GC / per) * per;
+            if (p < pieces && row < count) *reinterpret_cast<u32x4 *>(rows + (uint32_t)row * row_step + group) = x[i];
+        }
+    }
 
     __device__ inline void fetch(const ChunkArgs &A, int h, int first, int n_, size_t entry) {
         n = n_;
@@ -247,8 +278,10 @@ struct Producer {
     }
 
     // All of a producing thread's work on a sequence of nc chunks: step i is chunk i, or nc - 1 - i
-    // in the reverse pass.
-    __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry0) {
+    // in the reverse pass.  out: o (dv) from the first token and the workgroup's first column on, where it goes
+    // through LDS.
+    __device__ inline void run(const ChunkArgs &A, Shared &sh, int h, int t0, int t1, int nc, size_t entry0, raw *out,
+                               uint32_t row_step) {
         cg = tid % CG;
         tg = tid / CG;
         auto chunk = [&](int i) { return REV ? nc - 1 - i : i; };
@@ -256,6 +289,10 @@ struct Producer {
         auto get = [&](int i) {
             const int c = chunk(i);
             fetch(A, h, t0 + c * kC, min(t1 - t0 - c * kC, kC), entry(i));
+        };
+        auto put = [&](int i) {
+            const int c = chunk(i);
+            store_out(sh, out + (size_t)c * kC * row_step, row_step, t1 - t0 - c * kC);
         };
         auto get_t = [&](int i) {
             if constexpr (REV) tm.load(A.back[entry(i)].N, tid);
@@ -270,9 +307,15 @@ struct Producer {
             lds_barrier();               // half A of i stands; half B of i - 1 is done with
             write_b(sh);
             if (i + 1 < nc) get_t(i + 1);
+            if constexpr (Shared::OUT)
+                if (i > 0) put(i - 1);
             lds_barrier();               // half B of i stands; half A of i is done with
             if (i + 1 < nc) write_a(sh, (i + 1) & 1);
             if (i + 2 < nc) get(i + 2);
+        }
+        if constexpr (Shared::OUT) {
+            lds_barrier();               // the last rows stand
+            put(nc - 1);
         }
     }
 };

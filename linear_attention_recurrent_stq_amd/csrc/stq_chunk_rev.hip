@@ -80,14 +80,18 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
         if (nc == 0) return;
         Producer<DK, KEYVEC, BF16, kReverse> p;
         p.tid = threadIdx.x - 64 * 2 * NW;
-        p.run(A, sh, h, t0, t1, nc, entry0);
+        const uint32_t row_step = (uint32_t)(H * DV / 4);
+        p.run(A, sh, h, t0, t1, nc, entry0,
+              Shared::OUT ? static_cast<raw *>(A.dv) + (size_t)t0 * row_step + (size_t)h * (DV / 4) + part * Shared::GC
+                          : nullptr,
+              row_step);
         return;
     }
 
     const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4, mine = wave < NW ? wave : wave - NW;
     const int col0 = (part * NW + mine) * 16;
     // lane (g, c16) reads and writes columns 4 (c16 / 4) .. + 3 of rows 16 rt + 4 g + c16 % 4
-    const int row0 = 4 * g + (c16 & 3);
+    const int row0 = 4 * g + (c16 & 3), out0 = slab_at<Shared::GC>(row0, 4 * mine + (c16 >> 2));
     const uint32_t row_step = (uint32_t)(H * DV / 4);    // in groups of four columns
     const size_t col4 = (size_t)h * (DV / 4) + col0 / 4;
     const uint32_t lane4 = c16 >> 2;     // (offsets of a lane stay 32 bits, bases in scalar registers)
@@ -154,6 +158,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             columns_times<CT, NQ>(load_c, dh, dl, f, f2, [&](int ct, floatx4 z) { sh.zd[mine][ct][lane] = z * undo; });
             lds_barrier();
         }
+        if constexpr (Shared::OUT) lds_barrier();
         return;
     }
 
@@ -206,7 +211,8 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             quad_transpose(z);
             raw out;
             narrow(z, out);
-            if (16 * rt + at < n) dv[(uint32_t)(16 * rt + at) * row_step + lane4] = out;
+            if constexpr (Shared::OUT) sh.out[out0 + 16 * Shared::GC * rt] = out;
+            else if (16 * rt + at < n) dv[(uint32_t)(16 * rt + at) * row_step + lane4] = out;
         }
         store_tiles(A.y + entry * (kC * DV) + col0 * kC, y, 4);
         const float su = scale_to(column_max(R), 13, undo);
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__((64 * 2 * PassShared<DK, KEYVEC, BF16, kRevers
             for (int r = 0; r < 4; ++r) S[ct][r] = __builtin_fmaf(z[r], undo, __builtin_fmaf(S[ct][r], d[r], q[r]));
         });
     }
+    if (Shared::OUT && nc) lds_barrier();  // the last rows are stored
     if (!A.dinitial) return;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
