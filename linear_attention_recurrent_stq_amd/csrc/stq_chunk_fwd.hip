@@ -21,13 +21,13 @@
 // threads that fold the gates in then have too few registers, 407 against 468.)
 //
 // A workgroup takes 64 columns; the others of a head find its rows in the same XCD's L2.
-// Longest sequences start first.  v and o are read and written four columns of a row a lane, and
-// turned within quads of lanes.
+// Longest sequences start first.  v and o are read and written four columns of a row a lane (bf16
+// outputs by way of LDS), and turned within quads of lanes.
 //
 // Measured, bf16, d_k = d_v = 128, MI355X: scalar gates, 24 ragged sequences of 24000 tokens, 32
-// heads 492 us; key-vector gates, 40 of 16001 tokens, 32 heads 402 us.  One sequence of 16384
-// tokens, 16 heads, key-vector gates: 1063 us in one go (32 workgroups); in 5 segments 202 us for
-// the segments' states and matrices, 14 us to join them, 256 us for the outputs.
+// heads 461 us; key-vector gates, 40 of 16001 tokens, 32 heads 408 us.  One sequence of 16384
+// tokens, 16 heads, key-vector gates: 1063 us in one go (32 workgroups); in 5 segments 217 us for
+// the segments' states and matrices, 14 us to join them, 259 us for the outputs.
 
 #include "stq_chunk_pass.h"
 

@@ -27,8 +27,8 @@
 //
 // A workgroup holds about 117 KB of LDS and eight waves of 200 to 256 registers, so one a CU: the bound
 // is its vector instructions (49 % of the cycles with scalar gates, 57 % with key-vector ones) and
-// what they wait for. Measured, bf16, d_k = d_v = 128, 16 heads, MI355X: scalar gates, 16384 tokens 486 us
-// (887 MB, S and dS most of it: 1.8 TB/s); key-vector gates, 8192 tokens 360 us.
+// what they wait for. Measured, bf16, d_k = d_v = 128, 16 heads, MI355X: scalar gates, 16384 tokens 494 us
+// (887 MB, S and dS most of it: 1.8 TB/s); key-vector gates, 8192 tokens 359 us.
 
 #include "stq_chunk.h"
 

@@ -26,8 +26,8 @@
 // right operand in the registers it is in, so the chain needs no exchange.
 //
 // The bound is vector instructions (65 to 69 % of the cycles, the rest latency). Measured, bf16, d_k
-// 128, 32 heads, MI355X: scalar gates, 24000 tokens 214 us (478 MB: 2.2 TB/s); key-vector gates,
-// 16001 tokens 361 us (589 MB: 1.6 TB/s).
+// 128, 32 heads, MI355X: scalar gates, 24000 tokens 215 us (478 MB: 2.2 TB/s); key-vector gates,
+// 16001 tokens 361 to 377 us (589 MB: 1.6 TB/s).
 //
 // Rows past a chunk's last token repeat it, with beta 0 and gate 1: their rows and
 // columns of T are 0, and their outputs are not stored.

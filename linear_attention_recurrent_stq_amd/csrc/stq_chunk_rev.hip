@@ -10,9 +10,9 @@
 // y, dS; the helping waves form what does not depend on it, P^T dO and (Q G)^T dO, and hand it
 // over as result tiles in LDS.
 //
-// Measured, bf16, d_k = d_v = 128, 16 heads, MI355X: scalar gates, 8 ragged sequences of 16384 tokens 454 us,
+// Measured, bf16, d_k = d_v = 128, 16 heads, MI355X: scalar gates, 8 ragged sequences of 16384 tokens 426 us,
 // as long as the longest sequence's chain (about 7 us a step; the stores of dS, y and dV are 2 of
-// them); key-vector gates, 4 x 2048 tokens 177 us.
+// them); key-vector gates, 4 x 2048 tokens 171 us.
 
 #include "stq_chunk_pass.h"
 
